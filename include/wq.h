@@ -78,12 +78,18 @@ typedef enum wq_format {
     WQ_FMT_LLOYD8S = 1,
     /* [KM] §1.2, §2.2: code = centroid index 0..15, w = centroid; 16 fp16 centroids per
      * block of 64. aux = fp16 [n, k/64, 16]. */
-    WQ_FMT_LUT16 = 2
+    WQ_FMT_LUT16 = 2,
+    /* MXFP4, the 4-bit floating point of the OCP Microscaling Formats specification (v1.0):
+     * code = E2M1 (bit 3 the sign, bits 1-2 the exponent, bit 0 the mantissa: magnitudes
+     * 0, 0.5, 1, 1.5, 2, 3, 4, 6), w = level * 2^(s - 127), one E8M0 byte s per group of 32
+     * (255: the group is NaN). aux = uint8 [n, 16 * ceil(k / 512)]: the k/32 scale bytes of
+     * each row, padded to whole 16 bytes (the padding is never used). */
+    WQ_FMT_MXFP4 = 3
 } wq_format;
 
 typedef struct wq_weight {
     int32_t fmt;            /* wq_format */
-    int32_t group;          /* DYADIC4: 64 or 32; LLOYD8S: 32; LUT16: 64 */
+    int32_t group;          /* DYADIC4: 64 or 32; LLOYD8S: 32; LUT16: 64; MXFP4: 32 */
     int64_t n;              /* rows (outputs), >= 1 */
     int64_t k;              /* columns (inputs), >= 1, multiple of group */
     const uint8_t* packed;  /* [n, k/2]: byte j of a row = code[2j] | code[2j+1] << 4
@@ -147,6 +153,29 @@ wq_status wq_quantize_lloyd(const uint16_t* w, int64_t n, int64_t k, const wq_ll
                             uint8_t* codes, uint8_t* packed, void* codebook, uint8_t* params,
                             float* mse_trace, wq_stream stream);
 
+typedef enum wq_dtype {
+    WQ_BF16 = 0,
+    WQ_F32 = 1
+} wq_dtype;
+
+/* MXFP4 quantisation (OCP Microscaling Formats v1.0, section 6.3). For every block of 32
+ * consecutive values of a row with largest magnitude amax: scale byte s = 127 + max(-127,
+ * floor(log2 amax) - 2) (amax = 0: s = 0), code = E2M1(x * 2^(127 - s)), rounded to nearest
+ * with ties to the even code, magnitudes above 6 saturating at 6; a zero keeps its sign. A
+ * block that holds a NaN or an infinity gets s = 255 and codes 0 (all of it is NaN): here
+ * inputs need not be finite.
+ *   x       [n, k] of the given dtype; k % 32 == 0.
+ *   dtype   WQ_BF16 or WQ_F32.
+ *   scale   out uint8 [n, 16 * ceil(k / 512)] (padding written as 0), or NULL.
+ *   codes   out uint8 [n, k] (one code per byte), or NULL.
+ *   packed  out uint8 [n, k/2] (two codes per byte, see wq_weight), or NULL.
+ *   q       out [n, k] of the same dtype: level * 2^(s - 127), exact in both types (the
+ *           forward value of fake quantisation; its straight-through backward is the
+ *           identity and needs no call), or NULL.
+ * At least one of codes, packed and q must be non-NULL. Bit-exact (NaNs of q: any NaN). */
+wq_status wq_quantize_mxfp4(const void* x, int32_t dtype, int64_t n, int64_t k, uint8_t* scale,
+                            uint8_t* codes, uint8_t* packed, void* q, wq_stream stream);
+
 /* ------------------------------------------------------------------------------------ */
 /* Packing and reconstruction                                                            */
 /* ------------------------------------------------------------------------------------ */
@@ -161,7 +190,8 @@ wq_status wq_unpack(const uint8_t* packed, int64_t n, int64_t k, uint8_t* codes,
 /* Dense reconstruction of a packed weight ([DG] §2.5 unpack; [G32] §5.2; [KM] §2.2):
  *   DYADIC4 -> bf16(step * (idx - 8)), one rounding to nearest even;
  *   LLOYD8S -> bf16(+/- level[q]);
- *   LUT16   -> the fp16 centroid itself (out holds fp16 patterns).
+ *   LUT16   -> the fp16 centroid itself (out holds fp16 patterns);
+ *   MXFP4   -> bf16(level * 2^(s - 127)) (exact; infinite where it overflows, NaN for s = 255).
  *   out  [n, k] 16-bit patterns. Bit-exact. */
 wq_status wq_dequant(const wq_weight* w, uint16_t* out, wq_stream stream);
 
@@ -213,7 +243,7 @@ wq_status wq_gumbel_st_backward(const float* z, int64_t n, int64_t k, int32_t gr
 /* Decode-side W4A16 GEMV ([DG] §2.5/§3.2 fused unpack; [KM] §2.2, §4.1 small batch):
  * y[b, r] = sum_c Wdeq[r, c] * x[b, c], fp32 accumulation, bf16 output (rounded to
  * nearest even), for b < batch. Wdeq is the reconstruction wq_dequant gives (bf16 for
- * DYADIC4 / LLOYD8S; for LUT16 the fp16 centroid, multiplied by fp16 activations: each
+ * DYADIC4 / LLOYD8S / MXFP4; for LUT16 the fp16 centroid, multiplied by fp16 activations: each
  * batch row's chunk of x that a thread block stages is converted as x * 2^e, with the
  * power of two chosen from the chunk's largest |x| so that it lands in [2^15, 2^16), and
  * the chunk's fp32 sums are multiplied by 2^-e. Every finite bf16 x is in range; an
@@ -283,6 +313,7 @@ size_t wq_gemm_workspace_bytes(const wq_weight* w, int64_t m);
  * "materialized" bf16 path fused): y[i, r] = sum_c Wdeq[r, c] * x[i, c] for i < m, fp32
  * accumulation in tensor memory, bf16 output. Formats DYADIC4 (group 64 or 32), LLOYD8S
  * (the 8-level codebook plus sign of [G32] §5.2, rebuilt per stage from the group's levels)
+ * MXFP4 (the E2M1 level times the group's power of two, rebuilt per stage)
  * and LUT16 (the per-block-64 centroid table of [KM] §2.2, looked up per stage; the product
  * runs in fp16 on the activations converted into the workspace as x * 2^e per activation
  * row, the power of two chosen from the row's largest |x| as in wq_gemv_w4a16, and the
@@ -298,10 +329,52 @@ size_t wq_gemm_workspace_bytes(const wq_weight* w, int64_t m);
 wq_status wq_gemm_w4a16(const wq_weight* w, const uint16_t* x, int64_t m, uint16_t* y,
                         void* ws, size_t ws_bytes, wq_stream stream);
 
+/* Bytes of device workspace the _bf16 forms below need for the codes and scale bytes of m rows
+ * of k activations. */
+size_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t k);
+
+/* The product of two MXFP4 matrices on the block-scaled tensor cores (tcgen05 kind::mxf4):
+ * y[i, r] = sum_c Wdeq[r, c] * Xdeq[i, c] for i < m, both operands as wq_dequant gives them
+ * (without its overflow to infinity: products are taken scaled), fp32 accumulation, bf16
+ * output. From one activation row (a decode step: K is then split over a thread-block
+ * cluster) to any number.
+ *   w   [n, k], x [m, k]: MXFP4, x->n = m the activation rows; k % 64 == 0; m < 2^30.
+ *   y   out bf16 [m, n].
+ * A block whose scale byte is 255 makes its whole row of y (x's) or column (w's) NaN.
+ * Within 2e-3 * sum_c |Wdeq| |Xdeq| + half a bf16 ulp of the exact product. One kernel launch,
+ * no workspace, run-to-run identical. */
+wq_status wq_gemm_mxfp4(const wq_weight* w, const wq_weight* x, uint16_t* y, wq_stream stream);
+
+/* The same for bf16 activations x [m, k], which are quantised first, into the workspace, as
+ * wq_quantize_mxfp4 does (m < 2^30). The two kernels overlap: the product loads weights while
+ * the activations are quantised.
+ *   ws  device workspace of at least wq_gemm_mxfp4_workspace_bytes(m, k) bytes. */
+wq_status wq_gemm_mxfp4_bf16(const wq_weight* w, const uint16_t* x, int64_t m, uint16_t* y,
+                             void* ws, size_t ws_bytes, wq_stream stream);
+
+/* Products grouped by expert (a mixture-of-experts layer): the activation rows are sorted by
+ * expert, rows offsets[e] .. offsets[e + 1] - 1 belong to expert e, and
+ * y[i, r] = sum_c Wdeq[e n + r, c] * Xdeq[i, c] for those rows.
+ *   w        the experts' weights stacked: MXFP4 [experts * n, k] (w->n = experts * n).
+ *   experts  1 .. 65536, a divisor of w->n.
+ *   offsets  DEVICE int32 [experts + 1], non-decreasing, 0 <= offsets[0],
+ *            offsets[experts] <= m. Read on the device only. Experts may have no rows; rows
+ *            before offsets[0] and from offsets[experts] on belong to no expert, and their
+ *            rows of y are not written. Offsets outside [0, m] are clamped; decreasing or
+ *            overlapping ones give unspecified rows of y (never an access outside the buffers).
+ *   x        as for wq_gemm_mxfp4 (or _bf16): m rows.
+ *   y        out bf16 [m, n].
+ * Same tolerance as wq_gemm_mxfp4. The result of a row does not depend on the other rows. */
+wq_status wq_gemm_mxfp4_experts(const wq_weight* w, int32_t experts, const int32_t* offsets,
+                                const wq_weight* x, uint16_t* y, wq_stream stream);
+wq_status wq_gemm_mxfp4_experts_bf16(const wq_weight* w, int32_t experts, const int32_t* offsets,
+                                     const uint16_t* x, int64_t m, uint16_t* y, void* ws,
+                                     size_t ws_bytes, wq_stream stream);
+
 /* Reads and clears the library's device-side error words. Kernels that wait on the GPU
- * (the GEMM pipeline's mbarrier waits, the water-filled GEMV's waits for its staged bytes)
- * give up after a bounded time instead of hanging and record a nonzero code (the GEMV's
- * is 2100); the BF16X kernels record one when an overflow-table index would pass
+ * (the GEMM pipeline's mbarrier waits, the water-filled GEMV's waits for its staged bytes, the
+ * MXFP4 products' pipeline waits) give up after a bounded time instead of hanging and record
+ * a nonzero code (the GEMV's is 2100, the MXFP4 products' 2201 to 2206); the BF16X kernels record one when an overflow-table index would pass
  * ovf_bytes, and the water-filling kernels one when a block's width is outside 3..5 or its
  * bytes do not fit packed_bytes (2000 dequant, 2001 pack, 2002 GEMV; the access is skipped
  * in every case). *code receives the code (0 = none). Synchronous (copies three ints from

@@ -1,0 +1,259 @@
+"""MXFP4 on the GPU against the fp64 oracle: quantisation and reconstruction bit for bit, the
+W4A16 products and the block-scaled products within tolerance and exactly where every sum is."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import mx
+from _util import f32, matmul_tolerance, to_dev, to_dev_bits
+
+pytestmark = pytest.mark.gpu
+
+
+def weights(n, k, seed, lo=-6, hi=3):
+    """Codes and scale bytes drawn at random (scales 2^lo .. 2^hi, every code), padding at 255."""
+    g = np.random.default_rng(seed)
+    codes = g.integers(0, 16, (n, k), dtype=np.uint8)
+    scale = np.full((n, mx.pitch(k)), 255, np.uint8)
+    scale[:, :k // 32] = g.integers(127 + lo, 128 + hi, (n, k // 32))
+    return codes, scale
+
+
+def packed(wq, codes, scale):
+    n, k = codes.shape
+    return wq.PackedWeight(wq.FMT_MXFP4, 32, n, k, to_dev(codes[:, 0::2] | codes[:, 1::2] << 4), to_dev(scale))
+
+
+def acts(m, k, seed):
+    g = np.random.default_rng(seed)
+    return torch.from_numpy((g.standard_normal((m, k)) * np.exp(0.5 * g.standard_normal(k))).astype(np.float32)).bfloat16()
+
+
+def one_hot(m, k, seed):
+    """Rows of zeros with one 1 each, and its columns."""
+    at = np.random.default_rng(seed).integers(0, k, m)
+    x = np.zeros((m, k), np.float32)
+    x[np.arange(m), at] = 1.0
+    return torch.from_numpy(x).bfloat16(), at
+
+
+def check(y, xv, wv):
+    ref, bound = mx.product(xv, wv)
+    err = np.abs(f32(y) - ref)
+    assert (err <= matmul_tolerance(ref, bound)).all(), float((err / np.maximum(bound, 1e-300)).max())
+
+
+# --- quantisation ------------------------------------------------------------------------
+
+def check_quantise(wq, x):
+    codes, scale = mx.quantize(x.double().numpy())
+    pw, c = wq.quantize_mxfp4(x.cuda(), codes=True)
+    q, pw2 = wq.fake_quant_mxfp4(x.cuda(), packed=True)
+    assert np.array_equal(pw.aux.cpu().numpy(), scale)
+    assert np.array_equal(c.cpu().numpy(), codes)
+    assert np.array_equal(pw.packed.cpu().numpy(), codes[:, 0::2] | codes[:, 1::2] << 4)
+    assert torch.equal(pw2.packed, pw.packed) and torch.equal(pw2.aux, pw.aux)
+    v = mx.values(codes, scale)
+    assert q.dtype == x.dtype and np.array_equal(q.cpu().double().numpy(), v, equal_nan=True)
+    neg = ~np.isnan(v)
+    assert np.array_equal(np.signbit(q.cpu().float().numpy())[neg], np.signbit(v)[neg])
+    d = wq.dequant(pw)
+    assert np.array_equal(d.cpu().double().numpy(), v, equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n, k", [(1, 32), (1, 64), (3, 512), (5, 544), (7, 2080), (129, 96), (1000, 4096)])
+def test_quantise_shapes(wq, n, k, dtype):
+    g = np.random.default_rng(n * 7 + k)
+    x = g.standard_normal((n, k)) * np.exp2(g.integers(-8, 8, (n, 1)))
+    check_quantise(wq, torch.from_numpy(x.astype(np.float32)).to(dtype))
+
+
+def test_quantise_every_bf16_pattern(wq):
+    """Every bf16 value beside a largest one of each of its binade's neighbours."""
+    bits = np.arange(65536, dtype=np.uint16).reshape(-1, 16)
+    top = (bits & 0x7FFF).max(1, keepdims=True).astype(np.int64)
+    rows = []
+    for up in (0, 1, 2, 3, 5):
+        lead = np.minimum(top + (up << 7), 0x7F7F).astype(np.uint16)
+        rows.append(np.concatenate([bits, np.repeat(lead, 16, 1)], 1))
+    x = torch.from_numpy(np.concatenate(rows).view(np.int16)).view(torch.bfloat16)
+    check_quantise(wq, x.contiguous())
+
+
+def test_quantise_fp32_ties_and_ends(wq):
+    """Every midpoint and its neighbours at many scales, subnormals, the largest values, blocks
+    with NaN and infinities, zeros of both signs."""
+    mid = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32)
+    pts = np.concatenate([mid, np.nextafter(mid, np.float32(0)), np.nextafter(mid, np.float32(9)), mx.LEVELS[1:]])
+    pts = np.concatenate([pts, [4.0, 6.5, 7.99]]).astype(np.float32)[:31]
+    rows = []
+    for e in (-149, -140, -127, -126, -125, -100, -3, 0, 9, 90, 125):
+        with np.errstate(over="ignore", under="ignore"):
+            b = np.ldexp(np.concatenate([pts, [4.0]]).astype(np.float64), e).astype(np.float32)
+        rows += [b, -b]
+    z = np.zeros(32, np.float32)
+    rows += [z, -z]
+    for bad in (np.nan, np.inf, -np.inf):
+        b = np.ones(32, np.float32)
+        b[17] = bad
+        rows.append(b)
+    check_quantise(wq, torch.from_numpy(np.stack(rows)))
+
+
+def test_dequant_at_the_ends_of_the_scales(wq):
+    codes = np.tile(np.arange(16, dtype=np.uint8), (256, 2))
+    scale = np.zeros((256, 16), np.uint8)
+    scale[:, 0] = np.arange(256)
+    v = mx.values(codes, scale)
+    d = wq.dequant(packed(wq, codes, scale)).cpu().double().numpy()
+    v = np.where(np.abs(v) >= 2.0 ** 128, np.sign(v) * np.inf, v)      # past bf16's largest
+    assert np.array_equal(d, v, equal_nan=True)
+
+
+# --- W4A16 products ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("n, k", [(1, 32), (17, 96), (128, 256), (300, 2080), (1003, 544), (2048, 4096)])
+@pytest.mark.parametrize("m", [1, 3, 8, 9, 16])
+def test_gemv(wq, m, n, k):
+    codes, scale = weights(n, k, n + k)
+    x = acts(m, k, m)
+    check(wq.gemv(packed(wq, codes, scale), x.cuda()), x.double().numpy(), mx.values(codes, scale))
+
+
+@pytest.mark.parametrize("m, n, k", [(17, 130, 64), (33, 1003, 1088), (64, 256, 4096), (100, 300, 192),
+                                     (128, 512, 512), (129, 257, 576), (512, 1024, 2048), (600, 640, 320)])
+def test_gemm(wq, m, n, k):
+    codes, scale = weights(n, k, n + k)
+    x = acts(m, k, m)
+    check(wq.gemm(packed(wq, codes, scale), x.cuda()), x.double().numpy(), mx.values(codes, scale))
+
+
+@pytest.mark.parametrize("m", [1, 7, 16, 48, 128, 300])
+def test_w4a16_one_hot_is_exact_at_every_scale(wq, m):
+    n, k = 256, 512
+    codes, scale = weights(n, k, 5, lo=-127, hi=124)
+    x, at = one_hot(m, k, m)
+    y = wq.gemm(packed(wq, codes, scale), x.cuda())
+    assert np.array_equal(f32(y), mx.values(codes, scale)[:, at].T)
+
+
+def test_gemv_grouped_and_plan(wq):
+    shapes = [(100, 512), (64, 96), (700, 1056)]
+    ws, xs, refs = [], [], []
+    for i, (n, k) in enumerate(shapes):
+        codes, scale = weights(n, k, i)
+        ws.append(packed(wq, codes, scale))
+        x = acts(4, k, i)
+        xs.append(x.cuda())
+        refs.append((x.double().numpy(), mx.values(codes, scale)))
+    for y, r in zip(wq.gemv_grouped(ws, xs), refs):
+        check(y, *r)
+    ys = [torch.empty((4, n), dtype=torch.bfloat16, device="cuda") for n, _ in shapes]
+    plan = wq.GroupedGemv(ws, xs, ys)
+    plan()
+    torch.cuda.synchronize()
+    for y, r in zip(ys, refs):
+        check(y, *r)
+    plan.close()
+
+
+# --- block-scaled products ---------------------------------------------------------------
+
+@pytest.mark.parametrize("m", [1, 16, 17, 40, 70, 130, 300])
+def test_product_one_hot_is_exact(wq, m):
+    """x picks columns of W: the scale byte of every block of W, then of x, reaches its rows."""
+    n, k = 300, 1088
+    codes, scale = weights(n, k, 3, lo=-100, hi=90)
+    x, at = one_hot(m, k, m)
+    y = wq.gemm_mxfp4(packed(wq, codes, scale), x.cuda())
+    assert np.array_equal(f32(y), mx.values(codes, scale)[:, at].T)
+    # and the other way round: one-hot weights, every scale of the activations
+    xc, xs = weights(m, k, 4, lo=-100, hi=90)
+    w, at = one_hot(n, k, 9)
+    wc, wsc = mx.quantize(w.double().numpy())
+    y = wq.gemm_mxfp4(packed(wq, wc, wsc), packed(wq, xc, xs))
+    assert np.array_equal(f32(y), mx.values(xc, xs)[:, at])
+    assert wq.device_error() == 0
+
+
+@pytest.mark.parametrize("k", [64, 128, 192, 448, 512, 576, 1024, 2112, 4096])
+@pytest.mark.parametrize("m, n", [(1, 1), (1, 300), (5, 128), (16, 129), (31, 260), (64, 64), (65, 200)])
+def test_product(wq, m, n, k):
+    codes, scale = weights(n, k, n + k)
+    x = acts(m, k, m)
+    xc, xs = mx.quantize(x.double().numpy())
+    pw = packed(wq, codes, scale)
+    y = wq.gemm_mxfp4(pw, x.cuda())
+    check(y, mx.values(xc, xs), mx.values(codes, scale))
+    assert torch.equal(y, wq.gemm_mxfp4(pw, packed(wq, xc, xs)))
+    assert wq.device_error() == 0
+
+
+@pytest.mark.parametrize("m, n, k", [(127, 300, 832), (128, 128, 4096), (129, 500, 1088), (255, 129, 320),
+                                     (256, 256, 2048), (257, 1003, 2112), (1000, 640, 512), (4096, 384, 1024)])
+def test_product_large(wq, m, n, k):
+    codes, scale = weights(n, k, n + k)
+    x = acts(m, k, m)
+    xc, xs = mx.quantize(x.double().numpy())
+    check(wq.gemm_mxfp4(packed(wq, codes, scale), x.cuda()), mx.values(xc, xs), mx.values(codes, scale))
+    assert wq.device_error() == 0
+
+
+# --- grouped by expert -------------------------------------------------------------------
+
+def experts_ref(xv, wv, off, n):
+    y = np.zeros((xv.shape[0], n))
+    b = np.zeros((xv.shape[0], n))
+    for e in range(len(off) - 1):
+        r = slice(off[e], off[e + 1])
+        y[r], b[r] = mx.product(xv[r], wv[e * n:(e + 1) * n])
+    return y, b
+
+
+@pytest.mark.parametrize("counts, n, k", [
+    ([1], 128, 64), ([3], 100, 512), ([0, 1], 7, 64), ([1, 0, 0, 2], 130, 576), ([0, 0, 5, 0], 257, 128),
+    ([16, 17, 1, 0, 15, 33], 200, 1088), ([130, 0, 1, 257, 64], 300, 192), ([500, 3], 129, 1024),
+    ([1] * 70, 64, 256), ([0] * 40 + [2] + [0] * 30 + [9], 33, 320), ([300, 0, 290, 310], 384, 512),
+])
+def test_experts(wq, counts, n, k):
+    e, t = len(counts), sum(counts)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    codes, scale = weights(e * n, k, n + k)
+    x = acts(t, k, t)
+    xc, xs = mx.quantize(x.double().numpy())
+    pw = packed(wq, codes, scale)
+    y = wq.gemm_experts_mxfp4(pw, x.cuda(), to_dev(off))
+    ref, bound = experts_ref(mx.values(xc, xs), mx.values(codes, scale), off, n)
+    assert (np.abs(f32(y) - ref) <= matmul_tolerance(ref, bound)).all()
+    assert torch.equal(y, wq.gemm_experts_mxfp4(pw, packed(wq, xc, xs), to_dev(off)))
+    assert wq.device_error() == 0
+
+
+def test_experts_leave_other_rows_alone(wq):
+    """Rows before the first and behind the last expert's keep what they held, whatever x holds there."""
+    n, k, t = 200, 576, 50
+    off = np.array([7, 7, 20, 41], np.int32)
+    codes, scale = weights(3 * n, k, 1)
+    x = acts(t, k, 2)
+    x[:7] = float("nan")
+    x[41:] = float("inf")
+    out = torch.full((t, n), 3.5, dtype=torch.bfloat16, device="cuda")
+    y = wq.gemm_experts_mxfp4(packed(wq, codes, scale), x.cuda(), to_dev(off), out=out)
+    assert y is out and (y[:7] == 3.5).all() and (y[41:] == 3.5).all()
+    xc, xs = mx.quantize(np.nan_to_num(x.double().numpy(), posinf=0.0))
+    ref, bound = experts_ref(mx.values(xc, xs), mx.values(codes, scale), off, n)
+    r = slice(7, 41)
+    assert (np.abs(f32(y) - ref)[r] <= matmul_tolerance(ref, bound)[r]).all()
+
+
+def test_experts_with_no_rows_at_all(wq):
+    codes, scale = weights(4 * 64, 128, 1)
+    pw = packed(wq, codes, scale)
+    out = torch.full((9, 64), -2.0, dtype=torch.bfloat16, device="cuda")
+    wq.gemm_experts_mxfp4(pw, acts(9, 128, 1).cuda(), torch.full((5,), 4, dtype=torch.int32, device="cuda"), out=out)
+    assert (out == -2.0).all()
+    y = wq.gemm_experts_mxfp4(pw, torch.empty((0, 128), dtype=torch.bfloat16, device="cuda"),
+                              torch.zeros(5, dtype=torch.int32, device="cuda"))
+    assert y.shape == (0, 64)

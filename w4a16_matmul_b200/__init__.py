@@ -31,7 +31,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 # --- constants mirrored from include/wq.h -----------------------------------------------
 WQ_OK, WQ_EINVAL, WQ_EALIGN, WQ_EUNSUPPORTED, WQ_ECUDA, WQ_ETIMEOUT, WQ_EDATA = range(7)
-FMT_DYADIC4, FMT_LLOYD8S, FMT_LUT16 = 0, 1, 2
+FMT_DYADIC4, FMT_LLOYD8S, FMT_LUT16, FMT_MXFP4 = 0, 1, 2, 3
+BF16, F32 = 0, 1
 LLOYD_G32_WARM, LLOYD_KMEANS16 = 0, 1
 GEMV_MAX_GROUPED = 192
 
@@ -54,6 +55,12 @@ _SIG = {
     "wq_quantize_dyadic": ([_vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp], _i32),
     "wq_quantize_lloyd": ([_vp, _i64, _i64, ctypes.POINTER(WqLloydParams), _vp, _vp, _vp, _vp,
                            _vp, _vp], _i32),
+    "wq_quantize_mxfp4": ([_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp], _i32),
+    "wq_gemm_mxfp4_workspace_bytes": ([_i64, _i64], _sz),
+    "wq_gemm_mxfp4": ([_WP, _WP, _vp, _vp], _i32),
+    "wq_gemm_mxfp4_bf16": ([_WP, _vp, _i64, _vp, _vp, _sz, _vp], _i32),
+    "wq_gemm_mxfp4_experts": ([_WP, _i32, _vp, _WP, _vp, _vp], _i32),
+    "wq_gemm_mxfp4_experts_bf16": ([_WP, _i32, _vp, _vp, _i64, _vp, _vp, _sz, _vp], _i32),
     "wq_pack": ([_vp, _i64, _i64, _vp, _vp], _i32),
     "wq_fake_quant_ste": ([_vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp], _i32),
     "wq_gumbel_st_backward": ([_vp, _i64, _i64, _i32, _vp, ctypes.c_float, _vp, _vp, _vp, _vp], _i32),
@@ -157,7 +164,8 @@ class PackedWeight:
     n: int
     k: int
     packed: torch.Tensor          # uint8 [n, k/2]
-    aux: torch.Tensor             # bf16 [n, k/g] | fp32 [n, k/32, 8] | fp16 [n, k/64, 16]
+    aux: torch.Tensor             # bf16 [n, k/g] | fp32 [n, k/32, 8] | fp16 [n, k/64, 16] |
+                                  # MXFP4: uint8 [n, mx_pitch(k)], k/32 scale bytes a row
 
     def desc(self) -> WqWeight:
         return WqWeight(self.fmt, self.group, self.n, self.k, self.packed.data_ptr(), self.aux.data_ptr())
@@ -235,6 +243,45 @@ def quantize_lloyd(w: torch.Tensor, mode: int = LLOYD_G32_WARM, rounds: int = 25
     _check(_lib.wq_quantize_lloyd(_ptr(w), n, k, ctypes.byref(prm), _ptr(c), _ptr(p), _ptr(book),
                                   _ptr(params), _ptr(tr), _stream(w)))
     return PackedWeight(fmt, g, n, k, p, book), dict(codes=c, params=params, trace=tr)
+
+
+def mx_pitch(k: int) -> int:
+    """Bytes between the rows of an MXFP4 weight's scale bytes (k/32 padded to whole 16)."""
+    return (k + 511) // 512 * 16
+
+
+def _quantize_mx(x: torch.Tensor, codes: bool, packed: bool, q: bool):
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor (no CPU path)")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous [n, k] matrix")
+    n, k = x.shape
+    dev = x.device
+    s = torch.empty((n, mx_pitch(k)), dtype=torch.uint8, device=dev) if packed or codes else None
+    c = torch.empty((n, k), dtype=torch.uint8, device=dev) if codes else None
+    p = torch.empty((n, k // 2), dtype=torch.uint8, device=dev) if packed else None
+    v = torch.empty_like(x) if q else None
+    _check(_lib.wq_quantize_mxfp4(_ptr(x), F32 if x.dtype == torch.float32 else BF16, n, k, _ptr(s), _ptr(c),
+                                  _ptr(p), _ptr(v), _stream(x)))
+    return s, c, PackedWeight(FMT_MXFP4, 32, n, k, p, s) if packed else None, v
+
+
+def quantize_mxfp4(x: torch.Tensor, codes: bool = False):
+    """MXFP4 quantisation of a bf16 or fp32 [n, k] matrix, k % 32 == 0 (weights, or the
+    activations of gemm_mxfp4): E2M1 codes and one power-of-two scale byte per 32 columns.
+    Returns (PackedWeight, codes uint8 [n, k] | None)."""
+    _, c, pw, _ = _quantize_mx(x, codes, True, False)
+    return pw, c
+
+
+def fake_quant_mxfp4(z: torch.Tensor, packed: bool = False):
+    """The values MXFP4 gives z [n, k] (bf16 or fp32): the forward pass of a QAT step on latent
+    weights, whose straight-through backward is the identity. Returns (q like z,
+    PackedWeight | None)."""
+    _, _, pw, q = _quantize_mx(z, False, packed, True)
+    return q, pw
 
 
 def pack(codes: torch.Tensor) -> torch.Tensor:
@@ -376,6 +423,75 @@ def gemm_static(w: PackedWeight, x: torch.Tensor, out: torch.Tensor | None = Non
     d = w.desc()
     _check(_lib.wq_gemm_w4a16_static(ctypes.byref(d), _ptr(x), m, _ptr(y), _stream(x)))
     return y
+
+
+def _mx_product(w: PackedWeight, x, out, workspace, offsets):
+    coded = isinstance(x, PackedWeight)
+    if w.fmt != FMT_MXFP4 or (coded and x.fmt != FMT_MXFP4):
+        raise ValueError("w and x must be MXFP4 weights (or x a bf16 tensor)")
+    experts = 0
+    if offsets is not None:
+        _cuda(offsets, torch.int32, "offsets")
+        if offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError("offsets must be [experts + 1]")
+        experts = offsets.numel() - 1
+        if w.n % experts:
+            raise ValueError(f"the stack's {w.n} rows are not a multiple of {experts} experts")
+    n = w.n // experts if experts else w.n
+    if coded:
+        m, k, t = x.n, x.k, x.packed
+    else:
+        t = _cuda(x, torch.bfloat16, "x")
+        if x.dim() != 2:
+            raise ValueError("x must be [m, k]")
+        m, k = x.shape
+    if k != w.k:
+        raise ValueError(f"x has {k} columns, w has {w.k}")
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=t.device)
+    else:
+        _cuda(out, torch.bfloat16, "out")
+        if tuple(out.shape) != (m, n):
+            raise ValueError(f"out must be [{m}, {n}]")
+    if m == 0:
+        return out
+    d = w.desc()
+    if coded:
+        xd = x.desc()
+        if experts:
+            _check(_lib.wq_gemm_mxfp4_experts(ctypes.byref(d), experts, _ptr(offsets), ctypes.byref(xd), _ptr(out),
+                                              _stream(t)))
+        else:
+            _check(_lib.wq_gemm_mxfp4(ctypes.byref(d), ctypes.byref(xd), _ptr(out), _stream(t)))
+        return out
+    need = int(_lib.wq_gemm_mxfp4_workspace_bytes(m, k))
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=t.device)
+    if experts:
+        _check(_lib.wq_gemm_mxfp4_experts_bf16(ctypes.byref(d), experts, _ptr(offsets), _ptr(x), m, _ptr(out),
+                                               _ptr(workspace), need, _stream(t)))
+    else:
+        _check(_lib.wq_gemm_mxfp4_bf16(ctypes.byref(d), _ptr(x), m, _ptr(out), _ptr(workspace), need, _stream(t)))
+    return out
+
+
+def gemm_mxfp4(w: PackedWeight, x, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y = x W^T with both operands MXFP4, on the block-scaled tensor cores -> bf16 [m, n]. x is
+    quantize_mxfp4's result for [m, k] activations, or a bf16 [m, k] tensor, which is quantised
+    first (into `workspace` if given, see wq_gemm_mxfp4_workspace_bytes). k % 64 == 0."""
+    return _mx_product(w, x, out, workspace, None)
+
+
+def gemm_experts_mxfp4(w: PackedWeight, x, offsets: torch.Tensor, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """gemm_mxfp4 grouped by expert: w stacks the experts' weights ([experts * n, k]), the rows of
+    x are sorted by expert, and rows offsets[e] .. offsets[e + 1] - 1 (int32 on the device, never
+    read by the host) are multiplied with expert e's. Returns bf16 [m, n]; rows of no expert keep
+    what `out` held."""
+    if offsets is None:
+        raise ValueError("offsets must be a CUDA tensor")
+    return _mx_product(w, x, out, workspace, offsets)
 
 
 # --- BF16X lossless codec ------------------------------------------------------------------

@@ -104,6 +104,8 @@ wq_status check_weight(const wq_weight* w) {
         if (w->group != 32) return fail(WQ_EUNSUPPORTED, "LLOYD8S group must be 32 (got %d)", w->group);
     } else if (w->fmt == WQ_FMT_LUT16) {
         if (w->group != 64) return fail(WQ_EUNSUPPORTED, "LUT16 group must be 64 (got %d)", w->group);
+    } else if (w->fmt == WQ_FMT_MXFP4) {
+        if (w->group != 32) return fail(WQ_EUNSUPPORTED, "MXFP4 group must be 32 (got %d)", w->group);
     } else {
         return fail(WQ_EINVAL, "unknown weight format %d", w->fmt);
     }
@@ -173,13 +175,18 @@ wq_status wq_device_error(int32_t* code) {
     if (!code) return fail(WQ_EINVAL, "code is NULL");
     wq_status st = read_device_error(code);
     if (st) return st;
-    int32_t data = 0, wf = 0;
+    int32_t data = 0, wf = 0, mx = 0;
     if ((st = read_bf16x_error(&data))) return st;
     if ((st = read_wf_error(&wf))) return st;
+    if ((st = read_mx_error(&mx))) return st;
     if (*code != 0) return fail(WQ_ETIMEOUT, "a bounded device wait expired (code %d)", *code);
     if (data != 0) {
         *code = data;
         return fail(WQ_EDATA, "BF16X overflow index past ovf_bytes (code %d)", data);
+    }
+    if (mx != 0) {
+        *code = mx;
+        return fail(WQ_ETIMEOUT, "a wait of an MXFP4 product expired (code %d)", mx);
     }
     if (wf >= 2100) {
         *code = wf;
@@ -372,6 +379,22 @@ wq_status wq_quantize_lloyd(const uint16_t* w, int64_t n, int64_t k, const wq_ll
                            (cudaStream_t)stream);
 }
 
+wq_status wq_quantize_mxfp4(const void* x, int32_t dtype, int64_t n, int64_t k, uint8_t* scale,
+                            uint8_t* codes, uint8_t* packed, void* q, wq_stream stream) {
+    g_last_error[0] = 0;
+    if (dtype != WQ_BF16 && dtype != WQ_F32) return fail(WQ_EINVAL, "unknown dtype %d", dtype);
+    wq_status st = check_shape(n, k, 32);
+    if (st) return st;
+    if ((st = check_ptr(x, "x", false))) return st;
+    if ((st = check_ptr(scale, "scale", true))) return st;
+    if ((st = check_ptr(codes, "codes", true))) return st;
+    if ((st = check_ptr(packed, "packed", true))) return st;
+    if ((st = check_ptr(q, "q", true))) return st;
+    if (!codes && !packed && !q) return fail(WQ_EINVAL, "codes, packed and q are all NULL");
+    if ((st = check_injected())) return st;
+    return launch_quantize_mxfp4(x, dtype, n, k, scale, codes, packed, q, (cudaStream_t)stream);
+}
+
 wq_status wq_pack(const uint8_t* codes, int64_t n, int64_t k, uint8_t* packed, wq_stream stream) {
     g_last_error[0] = 0;
     wq_status st = check_shape(n, k, 0);
@@ -524,6 +547,99 @@ size_t wq_gemm_workspace_bytes(const wq_weight* w, int64_t m) {
 wq_status wq_gemm_w4a16(const wq_weight* w, const uint16_t* x, int64_t m, uint16_t* y, void* ws,
                         size_t ws_bytes, wq_stream stream) {
     return gemm_checked(w, x, m, y, ws, ws_bytes, (cudaStream_t)stream, kGemmTailScratch);
+}
+
+}  // extern "C"
+
+namespace {
+
+size_t mx_x_code_bytes(int64_t m, int64_t k) { return ((size_t)m * (size_t)(k / 2) + 255) & ~(size_t)255; }
+
+wq_status check_mx(const wq_weight* w, const char* name) {
+    if (!w) return fail(WQ_EINVAL, "%s descriptor is NULL", name);
+    if (w->fmt != WQ_FMT_MXFP4) return fail(WQ_EINVAL, "%s must be MXFP4 (got format %d)", name, w->fmt);
+    wq_status st = check_weight(w);
+    if (st) return st;
+    if (w->k % 64 != 0) return fail(WQ_EINVAL, "MXFP4 products need k %% 64 == 0 (k=%lld)", (long long)w->k);
+    return WQ_OK;
+}
+
+// What the MXFP4 products check alike: the weights, the experts (0: the dense product), the row
+// count and y.
+wq_status check_mx_product(const wq_weight* w, int32_t experts, const int32_t* offsets, int64_t m, const uint16_t* y) {
+    wq_status st = check_mx(w, "w");
+    if (st) return st;
+    if (experts != 0) {
+        if (experts < 1 || experts > 65536) return fail(WQ_EINVAL, "experts=%d outside 1..65536", experts);
+        if (w->n % experts != 0)
+            return fail(WQ_EINVAL, "the stack's %lld rows are not a multiple of %d experts", (long long)w->n, experts);
+        if ((st = check_ptr(offsets, "offsets", false))) return st;
+    }
+    if (m < 1 || m >= (1LL << 30)) return fail(WQ_EINVAL, "m=%lld outside 1..2^30-1", (long long)m);
+    return check_ptr(y, "y", false);
+}
+
+wq_status mx_product(const wq_weight* w, int32_t experts, const int32_t* offsets, const wq_weight* x, uint16_t* y,
+                     cudaStream_t s) {
+    g_last_error[0] = 0;
+    if (!x) return fail(WQ_EINVAL, "x descriptor is NULL");
+    wq_status st = check_mx_product(w, experts, offsets, x->n, y);
+    if (st) return st;
+    if ((st = check_mx(x, "x"))) return st;
+    if (x->k != w->k)
+        return fail(WQ_EINVAL, "x has k=%lld columns, w has %lld", (long long)x->k, (long long)w->k);
+    if ((st = check_injected())) return st;
+    const int e = experts ? experts : 1;
+    return launch_gemm_mxfp4(w->packed, (const uint8_t*)w->aux, x->packed, (const uint8_t*)x->aux, x->n, w->n / e, w->k,
+                             e, offsets, y, false, s);
+}
+
+wq_status mx_product_bf16(const wq_weight* w, int32_t experts, const int32_t* offsets, const uint16_t* x, int64_t m,
+                          uint16_t* y, void* ws, size_t ws_bytes, cudaStream_t s) {
+    g_last_error[0] = 0;
+    wq_status st = check_mx_product(w, experts, offsets, m, y);
+    if (st) return st;
+    if ((st = check_ptr(x, "x", false))) return st;
+    if ((st = check_ptr(ws, "ws", false))) return st;
+    const size_t need = wq_gemm_mxfp4_workspace_bytes(m, w->k);
+    if (ws_bytes < need)
+        return fail(WQ_EINVAL, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes, need);
+    if ((st = check_injected())) return st;
+    uint8_t* codes = (uint8_t*)ws;
+    uint8_t* scale = codes + mx_x_code_bytes(m, w->k);
+    if ((st = launch_quantize_mxfp4(x, WQ_BF16, m, w->k, scale, nullptr, codes, nullptr, s))) return st;
+    const int e = experts ? experts : 1;
+    return launch_gemm_mxfp4(w->packed, (const uint8_t*)w->aux, codes, scale, m, w->n / e, w->k, e, offsets, y, true, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t k) {
+    if (m < 1 || k < 1 || m >= (1LL << 30) || k > (1LL << 31) - 1) return 0;
+    return mx_x_code_bytes(m, k) + (size_t)m * (size_t)mx_pitch(k);
+}
+
+wq_status wq_gemm_mxfp4(const wq_weight* w, const wq_weight* x, uint16_t* y, wq_stream stream) {
+    return mx_product(w, 0, nullptr, x, y, (cudaStream_t)stream);
+}
+
+wq_status wq_gemm_mxfp4_bf16(const wq_weight* w, const uint16_t* x, int64_t m, uint16_t* y, void* ws, size_t ws_bytes,
+                             wq_stream stream) {
+    return mx_product_bf16(w, 0, nullptr, x, m, y, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+wq_status wq_gemm_mxfp4_experts(const wq_weight* w, int32_t experts, const int32_t* offsets, const wq_weight* x,
+                                uint16_t* y, wq_stream stream) {
+    if (experts == 0) { g_last_error[0] = 0; return fail(WQ_EINVAL, "experts=0 outside 1..65536"); }
+    return mx_product(w, experts, offsets, x, y, (cudaStream_t)stream);
+}
+
+wq_status wq_gemm_mxfp4_experts_bf16(const wq_weight* w, int32_t experts, const int32_t* offsets, const uint16_t* x,
+                                     int64_t m, uint16_t* y, void* ws, size_t ws_bytes, wq_stream stream) {
+    if (experts == 0) { g_last_error[0] = 0; return fail(WQ_EINVAL, "experts=0 outside 1..65536"); }
+    return mx_product_bf16(w, experts, offsets, x, m, y, ws, ws_bytes, (cudaStream_t)stream);
 }
 
 }  // extern "C"

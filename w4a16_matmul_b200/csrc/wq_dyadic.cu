@@ -346,6 +346,7 @@ wq_status launch_unpack(const uint8_t* packed, int64_t n, int64_t k, uint8_t* co
 }
 
 wq_status launch_dequant(const wq_weight& w, uint16_t* out, cudaStream_t s) {
+    if (w.fmt == WQ_FMT_MXFP4) return launch_dequant_mxfp4(w, out, s);
     const int64_t n_words = w.n * w.k / 8;
     const int grid = stream_grid(n_words);
     if (w.fmt == WQ_FMT_DYADIC4) {

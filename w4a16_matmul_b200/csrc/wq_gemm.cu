@@ -25,17 +25,15 @@
 // levels per 32 columns, 16 fp16 centroids per 64) arrive by TMA with each stage and the
 // reconstruction warps look the codes up in them. LUT16 runs an fp16 MMA, so that its
 // centroids enter the product unrounded: its activations are converted to fp16 once, into
-// the workspace, by a small kernel ahead of the GEMM.
+// the workspace, by a small kernel ahead of the GEMM. MXFP4 looks its codes up in the constant
+// E2M1 table and multiplies by the group's power of two.
 // Every wait on an mbarrier is bounded; a wait that expires records an error word on the
 // device (see wq_device_error) and the CTA skips the rest of its work, still releasing its
 // tensor memory.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <mutex>
 
-#include "wq_internal.cuh"
+#include "wq_tcgen05.cuh"
 
 namespace wq {
 
@@ -43,42 +41,27 @@ WQ_DEBUG_WORD(gemm)
 
 __device__ int g_device_error;     // 0, or the code of the first expired device wait
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static std::mutex mu;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!fn) {
+        cudaDriverEntryPointQueryResult q;
+        void* p = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = (PFN_cuTensorMapEncodeTiled_v12000)p;
+        else
+            cudaGetLastError();
+    }
+    return fn;
+}
+
 namespace {
 
 constexpr int BM = 128;            // weight rows per CTA (MMA M)
 // Columns per stage, KB: 64 (one 128-byte swizzle row of bf16) or 128 (two such tiles, used
 // when K % 128 == 0: twice the reconstruction work per stage for the same bookkeeping).
-
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar)) : "memory");
-}
-
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row atoms of 1024 bytes.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);   // start address
-    d |= (uint64_t)1 << 16;                               // leading offset (unused here)
-    d |= (uint64_t)(1024 >> 4) << 32;                     // stride between 8-row atoms
-    d |= (uint64_t)1 << 46;                               // descriptor version
-    d |= (uint64_t)2 << 61;                               // 128-byte swizzle
-    return d;
-}
-
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 ::"r"(smem_u32(bar)) : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-          "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
-}
 
 // bf16 of the 8 codes of one packed word, in column order: (c0,c1), (c2,c3), (c4,c5),
 // (c6,c7), each bf16(step * (idx - 8)) rounded once. A bf16 pattern below 0x0100 is worth
@@ -109,9 +92,9 @@ __device__ __forceinline__ uint4 dyadic_row8_f32(uint32_t w, float step) {
 // as 216 KB hold, up to 16. Tensor-memory slots (32 columns each, the reconstructed
 // weights of one stage) only need to cover reconstruction-to-MMA latency; for BN <= 64 the
 // allocation stays at 256 columns so that two CTAs can share an SM.
-// Weight formats of the kernel (template parameter F): the dyadic step, the LLOYD8S levels
-// or the LUT16 table.
-constexpr int kFDy = 0, kFLl = 1, kFLu = 2;
+// Weight formats of the kernel (template parameter F): the dyadic step, the LLOYD8S levels,
+// the LUT16 table or the MXFP4 scale byte.
+constexpr int kFDy = 0, kFLl = 1, kFLu = 2, kFMx = 3;
 
 template <int BN, int F = kFDy, int KB = 64>
 struct Smem {
@@ -149,20 +132,6 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
         ::"r"(tmem_d), "r"(tmem_a), "l"(db), "r"(idesc), "r"(accumulate));
 }
 
-// Stores 32 consecutive 32-bit columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-          "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-          "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
-          "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-          "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
-}
-
 #ifndef WQ_GEMM_RW
 #define WQ_GEMM_RW 4
 #endif
@@ -175,33 +144,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 constexpr int rw_for(int bn) { return bn >= 128 ? WQ_GEMM_RW : WQ_GEMM_RW_NARROW; }
 constexpr int threads_for(int bn) { return 64 + 128 * rw_for(bn); }
 
-// Stores NC (8, 16 or 32) consecutive 32-bit columns of this thread's tensor-memory lane.
-template <int NC>
-__device__ __forceinline__ void tmem_st_part(uint32_t taddr, const uint32_t* v) {
-    static_assert(NC == 8 || NC == 16 || NC == 32, "8, 16 or 32 columns");
-    if constexpr (NC == 32) {
-        tmem_st32(taddr, *reinterpret_cast<const uint32_t(*)[32]>(v));
-    } else if constexpr (NC == 16) {
-        asm volatile(
-            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-            "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-            ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-              "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-              "r"(v[15])
-            : "memory");
-    } else {
-        asm volatile(
-            "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-            ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-              "r"(v[7])
-            : "memory");
-    }
-}
-
 // F == kFLl: LLOYD8S weights (groups of 32, 8 fp32 levels each, loaded per stage by TMA
 // through tmap_l; `scale` unused). F == kFLu: LUT16 weights (groups of 64, 16 fp16 centroids
-// each, loaded the same way), with fp16 activations and an fp16 MMA. Otherwise DYADIC4 with
-// group G.
+// each, loaded the same way), with fp16 activations and an fp16 MMA. F == kFMx: MXFP4 weights
+// (groups of 32; `scale` holds the scale bytes, rows mx_pitch(K) apart). Otherwise DYADIC4
+// with group G.
 template <int BN, int G, bool PARTIAL, int F, int KB>
 __global__ void __launch_bounds__(threads_for(BN), 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_p,
@@ -283,7 +230,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
                                     kt * KB + 64 * j, m0 + h * (BN / XBOXES), &full_tma[s]);
                 tma_load_2d(stage_p(s), &tmap_p, kt * (KB / 2), n0, &full_tma[s]);
                 // both tables hold KB / 4 elements of a row per stage
-                if (F != kFDy) tma_load_2d(stage_l(s), &tmap_l, kt * (KB / 4), n0, &full_tma[s]);
+                if (LL || LU) tma_load_2d(stage_l(s), &tmap_l, kt * (KB / 4), n0, &full_tma[s]);
             }
         }
     } else if (warp == 1) {
@@ -339,6 +286,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
         const int n = n0 + i;
         const bool row_ok = n < N;
         const uint16_t* srow = scale + (size_t)(row_ok ? n : 0) * (K / G) + colbase / G;
+        static_assert(F != kFMx || (32 % (WPT * 8) == 0), "a thread's MXFP4 columns lie in one group of 32");
+        const uint8_t* mrow = (const uint8_t*)scale + (size_t)(row_ok ? n : 0) * mx_pitch(K) + colbase / 32;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
         // the scales of this thread's group(s), loaded kPre stages ahead (a ring of registers)
         constexpr int kPre = 4;
@@ -350,6 +299,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
                 ring0[u] = ldg_u16(srow + (kt0 + u) * (KB / G));
                 ring1[u] = SPAN2 ? ldg_u16(srow + (kt0 + u) * (KB / G) + 1) : ring0[u];
             }
+            if (F == kFMx && row_ok && u < nk) ring0[u] = __ldg(mrow + (kt0 + u) * (KB / 32));
         }
         bool live = true;
         int s = 0, a = 0;                                  // stage and slot of iteration it
@@ -364,6 +314,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
                     ring0[u] = ldg_u16(srow + (kt0 + it + kPre) * (KB / G));
                     ring1[u] = SPAN2 ? ldg_u16(srow + (kt0 + it + kPre) * (KB / G) + 1) : ring0[u];
                 }
+                if (F == kFMx && row_ok && it + kPre < nk) ring0[u] = __ldg(mrow + (kt0 + it + kPre) * (KB / 32));
                 // the packed tile has landed, and the MMAs that last read this tensor-memory
                 // slot (iteration it - SLOTS) have completed (with coupled rings the first
                 // implies the second: the TMA for this iteration was issued only after the
@@ -424,6 +375,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
                     for (int c = 0; c < WPT; ++c) {
                         lut16_lookup4(wv[c], lo, hi, v[4 * c], v[4 * c + 1]);
                         lut16_lookup4(wv[c] >> 16, lo, hi, v[4 * c + 2], v[4 * c + 3]);
+                    }
+                } else if constexpr (F == kFMx) {
+                    // level times the group's power of two, exact in bf16
+                    const uint32_t ms = mx_scale_pair(sc0);
+#pragma unroll
+                    for (int c = 0; c < WPT; ++c) {
+                        uint32_t r[4];
+                        mx4_word(wv[c], r);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[4 * c + j] = bf16x2_fma(r[j], ms, 0x80008000u);
                     }
                 } else {
                     const bool huge = ((sc0 & 0x7FFFu) >= 0x7D80u) || ((sc1 & 0x7FFFu) >= 0x7D80u);
@@ -567,22 +528,6 @@ __global__ void __launch_bounds__(256) debug_scan_x_kernel(const uint4* __restri
 // ---------------------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------------------
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::mutex mu;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!fn) {
-        cudaDriverEntryPointQueryResult q;
-        void* p = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = (PFN_cuTensorMapEncodeTiled_v12000)p;
-        else
-            cudaGetLastError();
-    }
-    return fn;
-}
 
 struct Plan {
     int bn, kb, splits, kt_per_split, grid_n, grid_m;
@@ -780,7 +725,7 @@ wq_status launch_gemm(const wq_weight& w, const uint16_t* x, int64_t m, uint16_t
         return launch_gemv(w.fmt, w.group, &prob, 1, M, s);
     }
     const Plan p = plan_for(M, N, K, w.fmt, tail_cap);
-    auto enc = encode_fn();
+    auto enc = tensor_map_encoder();
     if (!enc) return fail(WQ_ECUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
     const size_t need = gemm_workspace_bytes(w, m, tail_cap);
     if (need > 0 && (ws == nullptr || ws_bytes < need)) return fail(WQ_EINVAL, "workspace too small");
@@ -852,12 +797,13 @@ wq_status launch_gemm(const wq_weight& w, const uint16_t* x, int64_t m, uint16_t
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) return fail(WQ_ECUDA, "tensor map for LLOYD8S levels failed (%d)", (int)r);
     }
-    // the kernel's `scale`: DYADIC4 the bf16 scales; LUT16 the activation rows' factors
+    // the kernel's `scale`: DYADIC4 the bf16 scales; MXFP4 the scale bytes; LUT16 the activation rows' factors
     // (the centroids travel through tmap_l); LLOYD8S unused
     const uint16_t* sc = lut ? (const uint16_t*)xinv : (const uint16_t*)w.aux;
     wq_status st;
 #define WQ_BN(BNV, KBV)                                                                                   \
     st = (w.fmt == WQ_FMT_LLOYD8S) ? launch_plan<BNV, 32, kFLl, 64>(p, tx, tp, tl, sc, y, ws, M, N, K, s) \
+       : (w.fmt == WQ_FMT_MXFP4) ? launch_plan<BNV, 32, kFMx, KBV>(p, tx, tp, tl, sc, y, ws, M, N, K, s)  \
        : lut                     ? launch_plan<BNV, 64, kFLu, KBV>(p, tx, tp, tl, sc, y, ws, M, N, K, s)  \
        : (w.group == 64)         ? launch_plan<BNV, 64, kFDy, KBV>(p, tx, tp, tl, sc, y, ws, M, N, K, s)  \
                                  : launch_plan<BNV, 32, kFDy, KBV>(p, tx, tp, tl, sc, y, ws, M, N, K, s)

@@ -3,7 +3,8 @@
 // Reconstruction follows "MiniCPM5-1B 验证: 6× 压缩…" §2.2/§2.5 (dyadic: bf16(step*(idx-8)))
 // "K-Means量化技术…" §2.2 (LUT16: a 16-entry centroid table per block of 64) and
 // "int4-g32+warm 裸量化…" §5.2 (LLOYD8S: bf16(±level) from a group's 8 levels, the codebook
-// held in registers), fused into the product instead of written out as a dense matrix.
+// held in registers) and the OCP microscaling specification (MXFP4: a level of the constant
+// E2M1 table times the group's power of two, exact in bf16), fused into the product instead of written out as a dense matrix.
 //
 // Design (HBM-bound: 0.53 B per dyadic weight, 1 B per LUT16 weight; what stands between
 // the kernel and the memory roof is the instruction count and latency of the in-register
@@ -112,15 +113,16 @@ __device__ __forceinline__ void dyadic_pairs_scaled(uint32_t w, uint32_t c1, uin
     p[3] = bf16x2_fma(t & 0x00F000F0u, c2, d);
 }
 
-enum Kind { kDyadic64 = 0, kDyadic32 = 1, kLut16 = 2, kLloyd8 = 3 };
+enum Kind { kDyadic64 = 0, kDyadic32 = 1, kLut16 = 2, kLloyd8 = 3, kMx4 = 4 };
 
 // Per-lane state of one 256-column step for R 16-row blocks: the 32 bytes of rows g and
 // g+8 of each block, and their per-group parameters.
 template <int KIND, int R>
 struct Step {
     uint32_t w[R][2][8];
-    // dyadic: bf16 scales; LUT16: table words; LLOYD8S: the fp32 levels of two groups
-    uint32_t aux[R][2][KIND == kLut16 ? 8 : KIND == kLloyd8 ? 16 : 2];
+    // dyadic: bf16 scales; LUT16: table words; LLOYD8S: the fp32 levels of two groups; MXFP4:
+    // both groups' scale bytes in one word
+    uint32_t aux[R][2][KIND == kLut16 ? 8 : KIND == kLloyd8 ? 16 : KIND == kMx4 ? 1 : 2];
 };
 
 // A 128-bit weight load that does not allocate in L1.
@@ -178,6 +180,12 @@ __device__ __forceinline__ void load_step(Step<KIND, R>& st, const GemvProblem& 
                 // raw table words; split into byte planes at use
                 st.aux[r][h][0] = la.x; st.aux[r][h][1] = la.y; st.aux[r][h][2] = la.z; st.aux[r][h][3] = la.w;
                 st.aux[r][h][4] = lb.x; st.aux[r][h][5] = lb.y; st.aux[r][h][6] = lb.z; st.aux[r][h][7] = lb.w;
+            } else if (KIND == kMx4) {
+                // the scale bytes of groups kk/32 and kk/32 + 1; outside the matrix (codes 8, a
+                // zero there) scale 1, also in place of the padding behind an odd last group
+                uint32_t sb = 0x7F7Fu;
+                if (rl && h0) sb = ldg_u16((const uint8_t*)pb.aux + (size_t)row * mx_pitch(K) + kk / 32);
+                st.aux[r][h][0] = h1 ? sb : (sb & 0xFFu) | 0x7F00u;
             } else {
                 // rows or groups outside the matrix get scale 1.0 (their codes are 8, so their
                 // weights are 0) which keeps the step on the one-FMA path
@@ -251,6 +259,7 @@ __device__ __forceinline__ void compute_step_staged(const Step<KIND, R>& st, flo
     constexpr int J = (KIND == kDyadic32) ? 2 : 1;
     uint32_t c1[R][2][J], c2[R][2][J], dd[R][2][J];
     uint32_t plo[R][2][4], phi[R][2][4];
+    uint32_t ms[R][2][2];                               // MXFP4: the groups' scales as bf16 pairs
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -270,6 +279,9 @@ __device__ __forceinline__ void compute_step_staged(const Step<KIND, R>& st, flo
                     phi[r][h][2 * j] = prmt(b01, b23, 0x7531u);
                     phi[r][h][2 * j + 1] = prmt(b45, b67, 0x7531u);
                 }
+            } else if (KIND == kMx4) {
+                ms[r][h][0] = mx_scale_pair(st.aux[r][h][0] & 0xFFu);
+                ms[r][h][1] = mx_scale_pair(st.aux[r][h][0] >> 8);
             } else if (KIND == kLut16) {
                 const uint32_t* L = st.aux[r][h];
 #pragma unroll
@@ -302,6 +314,19 @@ __device__ __forceinline__ void compute_step_staged(const Step<KIND, R>& st, flo
                 lloyd8_lookup4(st.w[r][0][sub] >> 16, plo[r][0] + j, phi[r][0] + j, q0[2], q0[3]);
                 lloyd8_lookup4(st.w[r][1][sub], plo[r][1] + j, phi[r][1] + j, q1[0], q1[1]);
                 lloyd8_lookup4(st.w[r][1][sub] >> 16, plo[r][1] + j, phi[r][1] + j, q1[2], q1[3]);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    mma_bf16_16816(acc[r][nb], q0[0], q1[0], q0[1], q1[1], b[nb][0], b[nb][1]);
+                    mma_bf16_16816(acc[r][nb], q0[2], q1[2], q0[3], q1[3], b[nb][2], b[nb][3]);
+                }
+            } else if (KIND == kMx4) {
+                mx4_word(st.w[r][0][sub], q0);
+                mx4_word(st.w[r][1][sub], q1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {           // exact: a level times a power of two
+                    q0[j] = bf16x2_fma(q0[j], ms[r][0][sub >> 2], 0x80008000u);
+                    q1[j] = bf16x2_fma(q1[j], ms[r][1][sub >> 2], 0x80008000u);
+                }
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     mma_bf16_16816(acc[r][nb], q0[0], q1[0], q0[1], q1[1], b[nb][0], b[nb][1]);
@@ -385,7 +410,7 @@ __device__ __forceinline__ void compute_step_exact(const GemvProblem& pb, int ro
 // range the one-FMA reconstruction covers.
 template <int KIND, int R>
 __device__ __forceinline__ bool step_scales_in_range(const Step<KIND, R>& st) {
-    if (KIND == kLut16 || KIND == kLloyd8) return true;
+    if (KIND == kLut16 || KIND == kLloyd8 || KIND == kMx4) return true;
     bool ok = true;
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -406,8 +431,8 @@ __device__ __forceinline__ bool step_scales_in_range(const Step<KIND, R>& st) {
 // columns paired (0,4), (1,5), (2,6), (3,7); LUT16: fp16 in natural order, each batch row's
 // 256 columns of a step times the power of two 2^e that puts their largest magnitude in
 // [2^15, 2^16) (lut_x_exponent), with 2^-e in xf[b * ns + step] for the step's sums (a warp
-// stages exactly one row's step: its 32 consecutive 8-column blocks); LLOYD8S: bf16 in
-// natural order. Columns at or beyond K are zero. Stages steps [c0, c0 + ns) of all B rows
+// stages exactly one row's step: its 32 consecutive 8-column blocks); LLOYD8S and MXFP4:
+// bf16 in natural order. Columns at or beyond K are zero. Stages steps [c0, c0 + ns) of all B rows
 // with the whole CTA; returns (dyadic) whether some staged |x| reaches 2^64 or is not finite.
 template <int KIND, int THREADS>
 __device__ __forceinline__ bool stage_x(uint8_t* xs, const uint16_t* x, int B, int K, int c0,
@@ -448,7 +473,7 @@ __device__ __forceinline__ bool stage_x(uint8_t* xs, const uint16_t* x, int B, i
                     f.x = bf16x2_to_f16x2_scaled(v[u].x, s1, s2); f.y = bf16x2_to_f16x2_scaled(v[u].y, s1, s2);
                     f.z = bf16x2_to_f16x2_scaled(v[u].z, s1, s2); f.w = bf16x2_to_f16x2_scaled(v[u].w, s1, s2);
                 }
-            } else if (KIND == kLloyd8) {
+            } else if (KIND == kLloyd8 || KIND == kMx4) {
                 f = v[u];                               // bf16 in natural order
             } else {
                 // a half of magnitude bits m >= 0x5F80 (|x| >= 2^64, inf, NaN) carries into
@@ -607,7 +632,7 @@ gemv_kernel(const __grid_constant__ GemvParams<MAXP> prm) {
 #pragma unroll
                         for (int j = h; j < 4; j += 2) acc[r][nb][j] = fmaf(sacc[r][nb][j], f, acc[r][nb][j]);
                 }
-        } else if (KIND == kLloyd8 || (!xbad && __all_sync(0xFFFFFFFFu, step_scales_in_range<KIND, R>(st)))) {
+        } else if (KIND == kLloyd8 || KIND == kMx4 || (!xbad && __all_sync(0xFFFFFFFFu, step_scales_in_range<KIND, R>(st)))) {
             compute_step_staged<KIND, NB, R>(st, acc, xs0 + 512 * (s - c0), xs1 + 512 * (s - c0));
         } else {
             compute_step_exact<KIND, NB, R>(pb, row0, g, s * 256 + t * 64, N, K, B, acc);
@@ -839,13 +864,16 @@ wq_status prepare(int fmt, int group, const GemvProblem* probs, int count, int b
     for (int i = 0; i < count; ++i) { prm.prob[i] = probs[i]; rows16 += (probs[i].n + 15) / 16; }
     const bool two = batch > 8;
     const int kind = (fmt == WQ_FMT_LUT16) ? kLut16 : (fmt == WQ_FMT_LLOYD8S) ? kLloyd8
-                   : (group == 64 ? kDyadic64 : kDyadic32);
+                   : (fmt == WQ_FMT_MXFP4) ? kMx4 : (group == 64 ? kDyadic64 : kDyadic32);
     if (kind == kLut16)
         return two ? pick_split<kLut16, 2, MAXP>(pr, probs, count, rows16, batch)
                    : pick_split<kLut16, 1, MAXP>(pr, probs, count, rows16, batch);
     if (kind == kLloyd8)
         return two ? pick_split<kLloyd8, 2, MAXP>(pr, probs, count, rows16, batch)
                    : pick_split<kLloyd8, 1, MAXP>(pr, probs, count, rows16, batch);
+    if (kind == kMx4)
+        return two ? pick_split<kMx4, 2, MAXP>(pr, probs, count, rows16, batch)
+                   : pick_split<kMx4, 1, MAXP>(pr, probs, count, rows16, batch);
     if (kind == kDyadic64)
         return two ? pick_split<kDyadic64, 2, MAXP>(pr, probs, count, rows16, batch)
                    : pick_split<kDyadic64, 1, MAXP>(pr, probs, count, rows16, batch);

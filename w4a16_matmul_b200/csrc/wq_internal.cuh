@@ -173,6 +173,20 @@ wq_status launch_wf_gemv(const uint8_t* packed, int64_t packed_bytes, const uint
                          const uint16_t* x, int batch, uint16_t* y, cudaStream_t s);
 wq_status read_wf_error(int32_t* code);
 
+// MXFP4 (wq_mx.cu, wq_mx_gemm.cu). A row's scale bytes are padded to whole 16 bytes, so that
+// every row starts where a 128-bit load or a TMA box may.
+__host__ __device__ constexpr int64_t mx_pitch(int64_t k) { return (k + 511) / 512 * 16; }
+wq_status launch_quantize_mxfp4(const void* x, int dtype, int64_t n, int64_t k, uint8_t* scale, uint8_t* codes,
+                                uint8_t* packed, void* q, cudaStream_t s);
+wq_status launch_dequant_mxfp4(const wq_weight& w, uint16_t* out, cudaStream_t s);
+// y = x W^T for MXFP4 x [m, k] and W [experts * n, k]: rows [offsets[e], offsets[e + 1]) of x
+// with the n rows of expert e; offsets NULL (experts 1): all rows. `overlap`: the kernel may
+// start beside the one before it in the stream, which writes x's codes and nothing else it reads.
+wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t* xp, const uint8_t* xsc, int64_t m,
+                            int64_t n, int64_t k, int experts, const int32_t* offsets, uint16_t* y, bool overlap,
+                            cudaStream_t s);
+wq_status read_mx_error(int32_t* code);
+
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
@@ -343,6 +357,20 @@ __device__ __forceinline__ void lut16_lookup4(uint32_t s, const uint32_t* lo, co
     const uint32_t h = (prmt(hi[0], hi[1], s7) & ~m) | (prmt(hi[2], hi[3], s7) & m);
     p01 = prmt(l, h, 0x5140u);
     p23 = prmt(l, h, 0x7362u);
+}
+
+// The E2M1 levels of the 8 codes of one packed word as bf16 pairs in column order: the
+// LLOYD8S lookup in the constant table 0, 1/2, 1, 3/2, 2, 3, 4, 6.
+__device__ __forceinline__ void mx4_word(uint32_t w, uint32_t (&p)[4]) {
+    const uint32_t lo[2] = {0xC0800000u, 0xC0804000u}, hi[2] = {0x3F3F3F00u, 0x40404040u};
+    lloyd8_lookup4(w, lo, hi, p[0], p[1]);
+    lloyd8_lookup4(w >> 16, lo, hi, p[2], p[3]);
+}
+// (2^(s - 127), 2^(s - 127)) as a bf16 pair for the E8M0 byte s: 2^-127 is subnormal, and 255
+// stands for NaN. A level (two significant bits) times it is exact, or overflows as IEEE does.
+__device__ __forceinline__ uint32_t mx_scale_pair(uint32_t s) {
+    const uint32_t b = s << 7 | ((s == 0 || s == 255) ? 0x40u : 0u);
+    return b * 0x10001u;
 }
 
 // bf16x2 -> fp16x2 (round to nearest even; exact for |x| in [2^-14, 65504]).

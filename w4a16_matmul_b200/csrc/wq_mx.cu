@@ -1,0 +1,247 @@
+// wq_mx.cu -- MXFP4 quantisation and reconstruction: the OCP microscaling format of 4-bit
+// floating point, blocks of 32 consecutive values of a row with one power-of-two scale.
+//
+//   value = level(code) * 2^(s - 127),   level = 0, 1/2, 1, 3/2, 2, 3, 4, 6 by the code's low
+//   three bits (E2M1: two exponent bits, one mantissa bit), negative when its bit 3 is set.
+//
+// The scale of a block is the power of two that brings its largest magnitude into [4, 8):
+// s - 127 = floor(log2 amax) - 2, so s = max(E - 2, 0) with E the biased exponent field of
+// amax (8 bits in bf16 and fp32 alike; zero and subnormal maxima have E = 0). Multiplying a
+// value by 2^(127 - s) is exact (or underflows towards a value that codes to 0 anyway), and
+// the conversion to E2M1 rounds once: to nearest, ties to the even code, 6 at most.
+//
+// Both kernels are HBM streams: a thread owns 8 consecutive values (a quarter of a block),
+// its loads and stores are the widest the type allows, and a warp's accesses are contiguous.
+#include "wq_internal.cuh"
+
+namespace wq {
+namespace {
+
+constexpr int kThreads = 256;
+
+int stream_grid(int64_t items, int per_sm_blocks = 8) {
+    int64_t blocks = (items + kThreads - 1) / kThreads;
+    const int64_t cap = (int64_t)sm_count() * per_sm_blocks;
+    if (blocks > cap) blocks = cap;
+    return (int)(blocks < 1 ? 1 : blocks);
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// E2M1 codes of 8 values, value j in nibble j.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{ .reg .b8 a, b, c, d; "
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; "
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3; "
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; "
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7; "
+        "mov.b32 %0, {a, b, c, d}; }"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+__device__ __forceinline__ void ldg_v8(const float* p, uint32_t (&v)[8]) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void stg_v8(float* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// One chunk of 8 values as loaded: 4 words of bf16 pairs, or 8 words of fp32.
+template <bool F32>
+struct Chunk {
+    uint32_t w[F32 ? 8 : 4];
+};
+
+template <bool F32>
+__device__ __forceinline__ Chunk<F32> load_chunk(const void* x, int64_t c, bool live) {
+    Chunk<F32> r;
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.w[i] = 0;
+        if (live) ldg_v8((const float*)x + 8 * c, r.w);
+    } else {
+        const uint4 v = live ? ldg_nc_v4((const uint4*)x + c) : make_uint4(0, 0, 0, 0);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    }
+    return r;
+}
+
+// Quantises the chunk c of the calling thread (four consecutive lanes hold one block) and
+// stores what was asked for. I: the index type of chunks.
+template <bool F32, typename I>
+__device__ __forceinline__ void quantise_chunk(const Chunk<F32>& ch, bool live, I c, uint32_t kb, uint32_t pitch,
+                                               uint8_t* __restrict__ scale, uint2* __restrict__ codes,
+                                               uint32_t* __restrict__ packed, void* __restrict__ q) {
+    // the block's largest magnitude as bits: their order is the values' order, with the
+    // infinities and then the NaNs on top
+    uint32_t top;
+    float v[8];
+    if constexpr (F32) {
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            top = max(top, ch.w[i] & 0x7FFFFFFFu);
+            v[i] = __uint_as_float(ch.w[i]);
+        }
+    } else {
+        const uint32_t m = max_u16x2(max_u16x2(ch.w[0] & 0x7FFF7FFFu, ch.w[1] & 0x7FFF7FFFu),
+                                     max_u16x2(ch.w[2] & 0x7FFF7FFFu, ch.w[3] & 0x7FFF7FFFu));
+        top = max(m << 16, m & 0xFFFF0000u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(ch.w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(ch.w[i] & 0xFFFF0000u);
+        }
+    }
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const uint32_t field = top >> 23;
+    const bool bad = field == 255;                             // a NaN or an infinity in the block
+    const uint32_t s = bad ? 255u : field > 2 ? field - 2 : 0u;
+    const float inv = __uint_as_float((254u - min(s, 252u)) << 23);   // 2^(127 - s)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= inv;
+    const uint32_t p = bad ? 0u : e2m1x8(v);
+    if (!live) return;
+    if (packed) packed[c] = p;
+    if (codes) {
+        const uint32_t e = p & 0x0F0F0F0Fu, o = (p >> 4) & 0x0F0F0F0Fu;
+        codes[c] = make_uint2(prmt(e, o, 0x5140u), prmt(e, o, 0x7362u));
+    }
+    if (scale && (threadIdx.x & 3) == 0) {
+        const I b = c >> 2;
+        if (pitch == kb) {
+            scale[b] = (uint8_t)s;
+        } else {
+            const I row = b / kb;
+            const uint32_t col = (uint32_t)(b - row * kb);
+            uint8_t* sr = scale + (int64_t)row * pitch;
+            sr[col] = (uint8_t)s;
+            if (col == kb - 1)                                 // the padding of the row's scales
+                for (uint32_t i = kb; i < pitch; ++i) sr[i] = 0;
+        }
+    }
+    if (q) {
+        uint32_t o[4];
+        mx4_word(p, o);
+        const uint32_t sc = mx_scale_pair(s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = bf16x2_fma(o[i], sc, 0x80008000u);   // exact: 2 significant bits
+        if constexpr (F32) {
+            uint32_t f[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { f[2 * i] = o[i] << 16; f[2 * i + 1] = o[i] & 0xFFFF0000u; }
+            stg_v8((float*)q + 8 * (int64_t)c, f);
+        } else {
+            stg_cs_v4((uint4*)q + c, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+    }
+}
+
+template <bool F32, typename I>
+__global__ void __launch_bounds__(kThreads)
+quantize_mxfp4_kernel(const void* __restrict__ x, I n_chunks, uint32_t kb, uint32_t pitch,
+                      uint8_t* __restrict__ scale, uint2* __restrict__ codes, uint32_t* __restrict__ packed,
+                      void* __restrict__ q) {
+    constexpr int U = F32 ? 2 : 4;
+    // a kernel launched to overlap this one may start; it waits before it reads what this writes
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const I stride = (I)gridDim.x * blockDim.x * U;
+    const I lane = threadIdx.x & 31;
+    // a warp covers U consecutive runs of 32 chunks; a block never straddles n_chunks
+    for (I c0 = ((I)blockIdx.x * blockDim.x + (threadIdx.x & ~31u)) * U; c0 < n_chunks; c0 += stride) {
+        Chunk<F32> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const I c = c0 + 32 * u + lane;
+            v[u] = load_chunk<F32>(x, (int64_t)c, c < n_chunks);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const I c = c0 + 32 * u + lane;
+            quantise_chunk<F32, I>(v[u], c < n_chunks, c, kb, pitch, scale, codes, packed, q);
+        }
+    }
+}
+
+// bf16(level * 2^(s - 127)): one packed word (8 codes) a thread and trip.
+template <typename I>
+__global__ void __launch_bounds__(kThreads)
+dequant_mxfp4_kernel(const uint32_t* __restrict__ packed, const uint8_t* __restrict__ scale, I n_words, uint32_t kb,
+                     uint32_t pitch, uint4* __restrict__ out) {
+    constexpr int U = 4;
+    const I lane = threadIdx.x & 31;
+    const I stride = (I)gridDim.x * blockDim.x * U;
+    for (I base = ((I)blockIdx.x * blockDim.x + (threadIdx.x & ~31u)) * U; base < n_words; base += stride) {
+        uint32_t p[U], s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const I i = base + 32 * u + lane;
+            p[u] = s[u] = 0;
+            if (i < n_words) {
+                p[u] = __ldg(packed + i);
+                const I b = i >> 2, row = pitch == kb ? 0 : b / kb;
+                s[u] = __ldg(scale + (int64_t)b + (int64_t)row * (pitch - kb));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const I i = base + 32 * u + lane;
+            if (i >= n_words) break;
+            uint32_t o[4];
+            mx4_word(p[u], o);
+            const uint32_t sc = mx_scale_pair(s[u]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = bf16x2_fma(o[j], sc, 0x80008000u);
+            stg_cs_v4(out + i, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+    }
+}
+
+}  // namespace
+
+wq_status launch_quantize_mxfp4(const void* x, int dtype, int64_t n, int64_t k, uint8_t* scale, uint8_t* codes,
+                                uint8_t* packed, void* q, cudaStream_t s) {
+    const int64_t chunks = n * k / 8;
+    const int U = dtype == WQ_F32 ? 2 : 4;
+    const int grid = stream_grid((chunks + U - 1) / U);
+    const uint32_t kb = (uint32_t)(k / 32), pitch = (uint32_t)mx_pitch(k);
+    // 32-bit chunk indices while the last trip's c0 + stride stays below 2^32
+    const bool narrow = chunks + (int64_t)grid * kThreads * U < (int64_t)1 << 32;
+#define WQ_MXQ(F32, I)                                                                                     \
+    quantize_mxfp4_kernel<F32, I><<<grid, kThreads, 0, s>>>(x, (I)chunks, kb, pitch, scale, (uint2*)codes, \
+                                                            (uint32_t*)packed, q)
+    if (dtype == WQ_F32) {
+        if (narrow) WQ_MXQ(true, uint32_t); else WQ_MXQ(true, uint64_t);
+    } else {
+        if (narrow) WQ_MXQ(false, uint32_t); else WQ_MXQ(false, uint64_t);
+    }
+#undef WQ_MXQ
+    return check_launch("quantize_mxfp4");
+}
+
+wq_status launch_dequant_mxfp4(const wq_weight& w, uint16_t* out, cudaStream_t s) {
+    const int64_t words = w.n * w.k / 8;
+    const int grid = stream_grid((words + 3) / 4);
+    const uint32_t kb = (uint32_t)(w.k / 32), pitch = (uint32_t)mx_pitch(w.k);
+    if (words + (int64_t)grid * kThreads * 4 < (int64_t)1 << 32)
+        dequant_mxfp4_kernel<uint32_t><<<grid, kThreads, 0, s>>>((const uint32_t*)w.packed, (const uint8_t*)w.aux,
+                                                                 (uint32_t)words, kb, pitch, (uint4*)out);
+    else
+        dequant_mxfp4_kernel<uint64_t><<<grid, kThreads, 0, s>>>((const uint32_t*)w.packed, (const uint8_t*)w.aux,
+                                                                 (uint64_t)words, kb, pitch, (uint4*)out);
+    return check_launch("dequant_mxfp4");
+}
+
+}  // namespace wq

@@ -1,0 +1,472 @@
+// wq_mx_gemm.cu -- products of two MXFP4 matrices on the block-scaled tensor cores, dense and
+// grouped by expert.
+//
+//   y[t, r] = sum over blocks b of 32 columns of  2^(sx[t, b] - 127) 2^(sw[r, b] - 127)
+//             sum_{c in b} x4[t, c] w4[r, c]
+//
+// tcgen05.mma kind::mxf4.block_scale takes the packed 4-bit codes of both operands from shared
+// memory and their scale bytes from tensor memory, and accumulates in fp32. One CTA computes a
+// 128 (weight rows) x BN (activation rows) tile over a K range:
+//   warp 0     TMA producer: per stage of 256 columns the codes of the weight tile [128 x 128
+//              bytes] and of the activation tile [BN x 128 bytes], 128-byte swizzle; per 512
+//              columns the scale bytes of both [128 + BN rows x 16 bytes];
+//   warp 1     allocates tensor memory, and one lane issues the MMAs (K = 64 each);
+//   warps 2-5  move the scale bytes into tensor memory: the MMA wants the four bytes of row r's
+//              128 columns in lane r % 32 of column r / 32, in each of the four lane quarters,
+//              so each warp fills its own quarter; afterwards they drain the accumulator.
+// Grouped by expert, a CTA finds its expert and its rows from the offsets on the device: the
+// host reads nothing back, and launches as many row tiles as the worst distribution needs.
+// Rows of the activation tile past the expert's range belong to the next expert (or lie behind
+// the matrix, where TMA fills zeros): they fill accumulator columns that are not stored.
+// Where the row tiles alone leave SMs idle (few activation rows), a cluster of CL CTAs splits K
+// and meets in distributed shared memory; the partial sums are added in rank order.
+// Every wait on an mbarrier is bounded; a wait that expires records an error word on the device
+// (see wq_device_error) and the CTA skips the rest of its work, still releasing its tensor
+// memory.
+#include <algorithm>
+
+#include "wq_tcgen05.cuh"
+
+namespace wq {
+
+__device__ int g_mx_error;          // 0, or the code of the first expired device wait
+
+namespace {
+
+constexpr int BM = 128;             // weight rows per CTA (MMA M)
+constexpr int KB = 256;             // columns per stage: one 128-byte swizzle row of codes
+constexpr int kThreads = 192;
+
+template <int BN>
+struct Cfg {
+    static constexpr int A_BYTES = BM * KB / 2, B_BYTES = BN * KB / 2;
+    static constexpr int STAGE = A_BYTES + B_BYTES;              // a multiple of 1024
+    static constexpr int SC_BYTES = (BM + BN) * 16;
+    // BN = 256 fills an SM; narrower tiles leave room for two CTAs
+    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 3 : 4;
+    static constexpr int SSTAGES = STAGES / 2 + 1;
+    // tensor memory: the accumulator, then TSLOTS slots of the scale bytes of 512 columns, per
+    // 128 columns CH columns: 4 for the weight rows and BN / 32, rounded up to 4, for the
+    // activation rows
+    static constexpr int ACC_COLS = BN < 32 ? 32 : BN;
+    static constexpr int XC = BN / 32 > 0 ? BN / 32 : 1;
+    static constexpr int CH = 4 + (XC + 3) / 4 * 4;
+    static constexpr int SLOT_COLS = 4 * CH;
+    static constexpr int TSLOTS = BN <= 32 ? 3 : 4;
+    static constexpr int USED_COLS = ACC_COLS + TSLOTS * SLOT_COLS;
+    static constexpr uint32_t TMEM_COLS = USED_COLS <= 128 ? 128 : USED_COLS <= 256 ? 256 : 512;
+    static_assert(USED_COLS <= 512, "tensor memory");
+    static constexpr int BARS = 2 * STAGES + 2 * SSTAGES + 2 * TSLOTS + 1;
+    static constexpr int TOTAL = STAGES * STAGE + SSTAGES * SC_BYTES + BARS * 8 + 32 + 1024;   // + alignment slack
+    static_assert(TOTAL <= 227 * 1024, "shared memory");
+};
+
+// D[128 x BN] (+)= A B^T over 64 columns: codes through descriptors, scale bytes at the
+// tensor-memory columns sfa / sfb (the byte pair of these columns is named in idesc).
+__device__ __forceinline__ void umma_mxf4(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p; }"
+        ::"r"(tmem_d), "l"(da), "l"(db), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+struct MxTile {
+    int expert, t0, tend;            // expert (-1: none), first activation row, end of its rows
+};
+
+// The row tile `mt` of all experts' tiles in order (warp-collective): expert e has
+// ceil(rows / BN) tiles. Offsets are clamped to [0, M], so no access leaves the buffers
+// whatever they hold.
+template <int BN>
+__device__ __forceinline__ MxTile find_tile(const int32_t* __restrict__ offsets, int experts, int M, int mt) {
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int e0 = 0; e0 < experts; e0 += 32) {
+        const int e = e0 + lane;
+        int lo = 0, hi = 0;
+        if (e < experts) {
+            lo = min(max(__ldg(offsets + e), 0), M);
+            hi = min(max(__ldg(offsets + e + 1), lo), M);
+        }
+        const int tiles = (hi - lo + BN - 1) / BN;
+        int incl = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        const int total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        if (mt < before + total) {
+            const int f = __ffs(__ballot_sync(0xFFFFFFFFu, before + incl > mt)) - 1;
+            const int t0 = __shfl_sync(0xFFFFFFFFu, lo + (mt - (before + incl - tiles)) * BN, f);
+            lo = __shfl_sync(0xFFFFFFFFu, lo, f);
+            hi = __shfl_sync(0xFFFFFFFFu, hi, f);
+            return MxTile{t0 >= lo && t0 < hi ? e0 + f : -1, t0, hi};
+        }
+        before += total;
+    }
+    return MxTile{-1, 0, 0};
+}
+
+template <int BN, int CL, bool EXPERTS>
+__global__ void __launch_bounds__(kThreads, BN == 256 ? 1 : 2)
+mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_ws,
+               const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_xs,
+               const int32_t* __restrict__ offsets, int experts, uint16_t* __restrict__ y, int M, int N, int K,
+               int grid_n, int kt_per_split) {
+    using C = Cfg<BN>;
+    constexpr int STAGES = C::STAGES, SS = C::SSTAGES, TS = C::TSLOTS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* sc_smem = smem + STAGES * C::STAGE;
+    uint64_t* full = (uint64_t*)(sc_smem + SS * C::SC_BYTES);   // codes of a stage landed
+    uint64_t* empty = full + STAGES;                             // ... and read by their MMAs
+    uint64_t* sfull = empty + STAGES;                            // scale bytes of 512 columns landed
+    uint64_t* sempty = sfull + SS;                               // ... and read by the movers
+    uint64_t* tfull = sempty + SS;                               // scale bytes in tensor memory
+    uint64_t* tfree = tfull + TS;                                // ... and read by their MMAs
+    uint64_t* acc_full = tfree + TS;
+    uint32_t* s_tmem = (uint32_t*)(acc_full + 1);
+    int* s_abort = (int*)(s_tmem + 1);
+    int* s_tile = s_abort + 1;                                   // expert, t0, tend
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lin = (int)blockIdx.x;
+    const int n0 = (lin % grid_n) * BM;
+    const int crank = CL > 1 ? (int)cluster_rank() : 0;
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+        for (int s = 0; s < SS; ++s) { mbar_init(&sfull[s], 1); mbar_init(&sempty[s], 4); }
+        for (int s = 0; s < TS; ++s) { mbar_init(&tfull[s], 4); mbar_init(&tfree[s], 1); }
+        mbar_init(acc_full, 1);
+        *s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    MxTile tile{0, (lin / grid_n) * BN, M};
+    if (EXPERTS) {
+        if (warp == 0) {
+            tile = find_tile<BN>(offsets, experts, M, lin / grid_n);
+            if (lane == 0) { s_tile[0] = tile.expert; s_tile[1] = tile.t0; s_tile[2] = tile.tend; }
+        }
+        __syncthreads();
+        tile = MxTile{s_tile[0], s_tile[1], s_tile[2]};
+        if (tile.expert < 0) {                                   // (clusters are not used here)
+            // not to be complete before the kernel this launch overlaps
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            return;
+        }
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(s_tmem)), "r"(C::TMEM_COLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.fence::before_thread_sync;");
+    }
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;");
+    const uint32_t tmem = *s_tmem;
+    const int KT = (K + KB - 1) / KB;
+    const int kt0 = crank * kt_per_split;                        // even: scale stages do not straddle splits
+    const int nk = max(0, min(KT, kt0 + kt_per_split) - kt0);
+    const int t0 = tile.t0, tend = tile.tend;
+    const int w0 = tile.expert * N + n0;                         // first weight row of the tile in the stack
+
+    auto stage_a = [&](int s) { return smem + s * C::STAGE; };
+    auto stage_b = [&](int s) { return smem + s * C::STAGE + C::A_BYTES; };
+    auto stage_sc = [&](int s) { return sc_smem + s * C::SC_BYTES; };
+    auto dead = [&](int code) {
+        *(volatile int*)s_abort = 1;
+        atomicCAS(&g_mx_error, 0, code);
+    };
+
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        if (lane == 0) {
+            // the weights of the first stages: they do not depend on the kernel before this one
+            const int pre = min(nk, STAGES);
+            for (int i = 0; i < pre; ++i) {
+                if ((i & 1) == 0) {
+                    mbar_expect_tx(&sfull[i >> 1], C::SC_BYTES);
+                    tma_load_2d(stage_sc(i >> 1), &map_ws, ((kt0 + i) >> 1) * 16, w0, &sfull[i >> 1]);
+                }
+                mbar_expect_tx(&full[i], C::STAGE);
+                tma_load_2d(stage_a(i), &map_w, (kt0 + i) * (KB / 2), w0, &full[i]);
+            }
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            for (int i = 0; i < pre; ++i) {
+                if ((i & 1) == 0)
+                    tma_load_2d(stage_sc(i >> 1) + BM * 16, &map_xs, ((kt0 + i) >> 1) * 16, t0, &sfull[i >> 1]);
+                tma_load_2d(stage_b(i), &map_x, (kt0 + i) * (KB / 2), t0, &full[i]);
+            }
+            int s = 0, ss = ((STAGES + 1) / 2) % SS;
+            uint32_t ph = 1, sph = (STAGES + 1) / 2 >= SS ? 1 : 0;   // parity of the stage's use
+            int i = pre;
+            for (; i < nk; ++i) {
+                if ((i & 1) == 0) {
+                    if (!mbar_wait(&sempty[ss], sph ^ 1, s_abort)) { dead(2201); break; }
+                    mbar_expect_tx(&sfull[ss], C::SC_BYTES);
+                    tma_load_2d(stage_sc(ss), &map_ws, ((kt0 + i) >> 1) * 16, w0, &sfull[ss]);
+                    tma_load_2d(stage_sc(ss) + BM * 16, &map_xs, ((kt0 + i) >> 1) * 16, t0, &sfull[ss]);
+                    if (++ss == SS) { ss = 0; sph ^= 1; }
+                }
+                if (!mbar_wait(&empty[s], ph ^ 1, s_abort)) { dead(2202); break; }
+                mbar_expect_tx(&full[s], C::STAGE);
+                tma_load_2d(stage_a(s), &map_w, (kt0 + i) * (KB / 2), w0, &full[s]);
+                tma_load_2d(stage_b(s), &map_x, (kt0 + i) * (KB / 2), t0, &full[s]);
+                if (++s == STAGES) { s = 0; ph ^= 1; }
+            }
+            if (i < nk) {
+                // gave up: the copies in flight must land before the CTA may end
+                const int got_s = (i + 2) / 2;                    // scale stages asked for, at most
+                for (int j = max(0, i - STAGES); j < i; ++j) mbar_wait(&full[j % STAGES], (j / STAGES) & 1);
+                for (int j = max(0, got_s - SS); j < got_s; ++j) mbar_wait(&sfull[j % SS], (j / SS) & 1);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0) {
+            // E2M1 codes (format 1) in both operands, E8M0 scales, fp32 accumulator
+            constexpr uint32_t idesc0 = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | (1u << 23) |
+                                        ((uint32_t)(BM >> 4) << 24);
+            int s = 0, t = 0;
+            uint32_t ph = 0, tph = 0;
+            for (int i = 0; i < nk; ++i) {
+                if ((i & 1) == 0 && !mbar_wait(&tfull[t], tph, s_abort)) { dead(2203); break; }
+                if (!mbar_wait(&full[s], ph, s_abort)) { dead(2204); break; }
+                asm volatile("tcgen05.fence::after_thread_sync;");
+                const uint64_t da = sw128_desc(smem_u32(stage_a(s))), db = sw128_desc(smem_u32(stage_b(s)));
+                const uint32_t sf = tmem + (uint32_t)(C::ACC_COLS + t * C::SLOT_COLS + (i & 1) * 2 * C::CH);
+                const int left = (K - (kt0 + i) * KB) / 64;       // K is a multiple of 64
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j < left) {
+                        // 64 codes are 32 bytes of the swizzle row: + 2 in descriptor units; bytes
+                        // 0-1 or 2-3 of the scale words
+                        const uint32_t id = (uint32_t)(j & 1) * 2u;
+                        const uint32_t sfa = sf + (uint32_t)((j >> 1) * C::CH);
+                        umma_mxf4(tmem, da + 2 * j, db + 2 * j, idesc0 | id << 4 | id << 29, sfa, sfa + 4,
+                                  (i > 0 || j > 0) ? 1u : 0u);
+                    }
+                }
+                umma_commit(&empty[s]);                           // fire once these MMAs are done
+                if (++s == STAGES) { s = 0; ph ^= 1; }
+                if ((i & 1) || i + 1 == nk) {
+                    umma_commit(&tfree[t]);
+                    if (++t == TS) { t = 0; tph ^= 1; }
+                }
+            }
+            // a commit also after giving up: it fires once every MMA issued so far is done, so
+            // tensor memory is never freed under a running MMA
+            umma_commit(acc_full);
+        }
+    } else {
+        // ---------------- scale bytes into tensor memory, then the epilogue ----------------
+        const int q = warp & 3;                                   // this warp's lane quarter
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+        int ss = 0, t = 0;
+        uint32_t sph = 0, tph = 0;
+        const int nt = (nk + 1) / 2;
+        for (int it = 0; it < nt; ++it) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sfull[ss], sph, s_abort) &&
+                                         (it < TS || mbar_wait(&tfree[t], tph ^ 1, s_abort)))) {
+                dead(2205); break;
+            }
+            const uint4* sc = (const uint4*)stage_sc(ss);
+            uint32_t v[C::SLOT_COLS];
+#pragma unroll
+            for (int j = 0; j < C::SLOT_COLS; ++j) v[j] = 0;
+#pragma unroll
+            for (int j = 0; j < 4 + C::XC; ++j) {                 // 32 rows each: the weights', then the activations'
+                uint4 r = make_uint4(0, 0, 0, 0);
+                if (BN >= 32 || j < 4 || lane < BN) r = sc[32 * j + lane];
+                v[j] = r.x; v[C::CH + j] = r.y; v[2 * C::CH + j] = r.z; v[3 * C::CH + j] = r.w;
+            }
+            const uint32_t dst = lane_base + (uint32_t)(C::ACC_COLS + t * C::SLOT_COLS);
+            tmem_st_part<32>(dst, v);
+            if constexpr (C::SLOT_COLS == 48) tmem_st_part<16>(dst + 32, v + 32);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) { mbar_arrive(&sempty[ss]); mbar_arrive(&tfull[t]); }
+            if (++ss == SS) { ss = 0; sph ^= 1; }
+            if (++t == TS) { t = 0; tph ^= 1; }
+        }
+        const bool drain = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0)) &&
+                           !__any_sync(0xFFFFFFFFu, *(volatile int*)s_abort != 0);
+        if (drain) {
+            asm volatile("tcgen05.fence::after_thread_sync;");
+            const int i = 32 * q + lane, n = n0 + i;
+#pragma unroll 1
+            for (int c0 = 0; c0 < BN; c0 += 16) {
+                uint32_t v[16];
+                if (CL == 1 && t0 + c0 >= tend) break;            // (the same for the whole CTA)
+                tmem_ld16(lane_base + (uint32_t)c0, v);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    if (CL > 1)                                   // the stages are free: partial sums [BN][BM]
+                        ((float*)smem)[(c0 + j) * BM + i] = nk > 0 ? __uint_as_float(v[j]) : 0.f;
+                    else if (n < N && t0 + c0 + j < tend)
+                        y[(size_t)(t0 + c0 + j) * N + n] = (uint16_t)float_to_bf16_bits(__uint_as_float(v[j]));
+                }
+            }
+        } else {
+            dead(2206);
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;");
+    __syncwarp();
+    if (CL > 1) {
+        cluster_sync();                                           // every rank's partial sums are in place
+        if (warp >= 2) {
+            const int i = (int)threadIdx.x - 64, n = n0 + i;
+            if (n < N)
+                for (int c = crank; c < BN && t0 + c < tend; c += CL) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int r = 0; r < CL; ++r) sum += ld_cluster_f32(smem_u32(smem) + (uint32_t)(c * BM + i) * 4, r);
+                    y[(size_t)(t0 + c) * N + n] = (uint16_t)float_to_bf16_bits(sum);
+                }
+        }
+        cluster_sync();                                           // ... and read
+    }
+    __syncthreads();
+    if (warp == 1) {
+        asm volatile("tcgen05.fence::after_thread_sync;");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------------------
+
+struct Maps {
+    CUtensorMap w, ws, x, xs;
+};
+
+wq_status encode_u8(CUtensorMap* map, const void* base, int64_t row_bytes, int64_t rows, int box_bytes, int box_rows,
+                    bool swizzle, const char* what) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return fail(WQ_ECUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+    cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows};
+    cuuint32_t es[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void*)base, dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(WQ_ECUDA, "tensor map for %s failed (%d)", what, (int)r);
+    return WQ_OK;
+}
+
+template <int BN, int CL, bool EXPERTS>
+wq_status launch_one(const Maps& mp, const int32_t* offsets, int experts, uint16_t* y, int M, int N, int K,
+                     int grid_n, int64_t grid_m, int kt_per_split, bool overlap, cudaStream_t s) {
+    auto k = mx_gemm_kernel<BN, CL, EXPERTS>;
+    constexpr int smem = Cfg<BN>::TOTAL;
+    static bool raised = false;        // the shared-memory opt-in holds for the process
+    if (!raised && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess)
+        raised = true;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(grid_n * grid_m), CL, 1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    if (CL > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = 1;
+        attr[na].val.clusterDim.y = CL;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    if (overlap) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na].val.programmaticStreamSerializationAllowed = 1;
+        ++na;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    cudaLaunchKernelEx(&cfg, k, mp.w, mp.ws, mp.x, mp.xs, offsets, experts, y, M, N, K, grid_n, kt_per_split);
+    return check_launch("mxfp4 gemm");
+}
+
+}  // namespace
+
+wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t* xp, const uint8_t* xsc, int64_t m,
+                            int64_t n, int64_t k, int experts, const int32_t* offsets, uint16_t* y, bool overlap,
+                            cudaStream_t s) {
+    const int M = (int)m, N = (int)n, K = (int)k;
+    const int grid_n = (N + BM - 1) / BM;
+    const int KT = (K + KB - 1) / KB;
+    const int sms = sm_count();
+    // activation rows a tile should hold: all of them, or the rows of a typical expert
+    const int64_t rows = offsets ? (m + experts - 1) / experts : m;
+    const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    // row tiles: with experts the most that any distribution of the rows needs
+    const int64_t grid_m = offsets ? m / bn + std::min<int64_t>(experts, m) : (m + bn - 1) / bn;
+    if (grid_m * grid_n > 0x7FFFFFFF) return fail(WQ_EUNSUPPORTED, "more than 2^31 - 1 tiles");
+    // K split over a cluster while the tiles leave SMs idle and every rank keeps 512 columns
+    int cl = 1;
+    if (!offsets && bn <= 64)
+        while (cl < 8 && grid_m * grid_n * cl * 2 <= 2 * (int64_t)sms && KT / (cl * 2) >= 2) cl *= 2;
+    int per = (KT + cl - 1) / cl;
+    per += per & 1;
+    Maps mp;
+    const int64_t pitch = mx_pitch(k);
+    wq_status st;
+    if ((st = encode_u8(&mp.w, wp, k / 2, n * experts, KB / 2, BM, true, "the weight codes"))) return st;
+    if ((st = encode_u8(&mp.ws, wsc, pitch, n * experts, 16, BM, false, "the weight scales"))) return st;
+    if ((st = encode_u8(&mp.x, xp, k / 2, m, KB / 2, bn, true, "the activation codes"))) return st;
+    if ((st = encode_u8(&mp.xs, xsc, pitch, m, 16, bn, false, "the activation scales"))) return st;
+#define WQ_MX(BN, CL, EX) \
+    launch_one<BN, CL, EX>(mp, offsets, experts, y, M, N, K, grid_n, grid_m, per, overlap, s)
+#define WQ_MX_CL(BN) \
+    (offsets ? WQ_MX(BN, 1, true) : cl == 8 ? WQ_MX(BN, 8, false) : cl == 4 ? WQ_MX(BN, 4, false) \
+             : cl == 2 ? WQ_MX(BN, 2, false) : WQ_MX(BN, 1, false))
+    switch (bn) {
+        case 16: return WQ_MX_CL(16);
+        case 32: return WQ_MX_CL(32);
+        case 64: return WQ_MX_CL(64);
+        case 128: return offsets ? WQ_MX(128, 1, true) : WQ_MX(128, 1, false);
+        default: return offsets ? WQ_MX(256, 1, true) : WQ_MX(256, 1, false);
+    }
+#undef WQ_MX_CL
+#undef WQ_MX
+}
+
+wq_status read_mx_error(int32_t* code) {
+    int v = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(&v, g_mx_error, sizeof v);
+    if (e != cudaSuccess) return fail(WQ_ECUDA, "reading the device error word: %s", cudaGetErrorString(e));
+    if (v != 0) {
+        const int zero = 0;
+        cudaMemcpyToSymbol(g_mx_error, &zero, sizeof zero);
+    }
+    *code = v;
+    return WQ_OK;
+}
+
+}  // namespace wq
