@@ -151,7 +151,7 @@ def _own(s):
         return q, coded.aux[:, :s["k"] // 32]
     w = wq.PackedWeight(wq.FMT_MXFP4, 32, s["packed"].shape[0], s["k"], s["packed"], s["scale"])
     if s["op"] == "weights":
-        return wq.gemm(w, s["x"])
+        return wq.gemv(w, s["x"]) if s["m"] <= 16 else wq.gemm(w, s["x"])
     if s["op"] == "product":
         return wq.gemm_mxfp4(w, s["x"])
     return wq.gemm_experts_mxfp4(w, s["x"], s["offsets"])
