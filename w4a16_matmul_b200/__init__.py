@@ -10,6 +10,7 @@ a CUDA device. PyTorch supplies device memory and the current stream only.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from dataclasses import dataclass
@@ -133,12 +134,14 @@ def debug_fail_next_launches(count: int) -> None:
     _lib.wq_debug_fail_next_launches(count)
 
 
-def _stream(t: torch.Tensor | None = None):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device if t is not None else None).cuda_stream)
+def _stream(t: torch.Tensor):
+    """The current stream of t's device, as the address ctypes passes on (the Stream object of
+    torch.cuda.current_stream() costs 2 us a call to make)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _cuda(t: torch.Tensor, dtype, name: str) -> torch.Tensor:
@@ -259,9 +262,10 @@ def _quantize_mx(x: torch.Tensor, codes: bool, packed: bool, q: bool):
         raise ValueError("x must be a contiguous [n, k] matrix")
     n, k = x.shape
     dev = x.device
-    s = torch.empty((n, mx_pitch(k)), dtype=torch.uint8, device=dev) if packed or codes else None
-    c = torch.empty((n, k), dtype=torch.uint8, device=dev) if codes else None
-    p = torch.empty((n, k // 2), dtype=torch.uint8, device=dev) if packed else None
+    u8 = torch.uint8
+    s = torch.empty((n, mx_pitch(k)), dtype=u8, device=dev) if packed or codes else None
+    c = torch.empty((n, k), dtype=u8, device=dev) if codes else None
+    p = torch.empty((n, k // 2), dtype=u8, device=dev) if packed else None
     v = torch.empty_like(x) if q else None
     _check(_lib.wq_quantize_mxfp4(_ptr(x), F32 if x.dtype == torch.float32 else BF16, n, k, _ptr(s), _ptr(c),
                                   _ptr(p), _ptr(v), _stream(x)))
@@ -425,6 +429,11 @@ def gemm_static(w: PackedWeight, x: torch.Tensor, out: torch.Tensor | None = Non
     return y
 
 
+@functools.lru_cache(maxsize=4096)
+def _mx_workspace_bytes(m: int, k: int) -> int:
+    return int(_lib.wq_gemm_mxfp4_workspace_bytes(m, k))
+
+
 def _mx_product(w: PackedWeight, x, out, workspace, offsets):
     coded = isinstance(x, PackedWeight)
     if w.fmt != FMT_MXFP4 or (coded and x.fmt != FMT_MXFP4):
@@ -448,7 +457,7 @@ def _mx_product(w: PackedWeight, x, out, workspace, offsets):
     if k != w.k:
         raise ValueError(f"x has {k} columns, w has {w.k}")
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=t.device)
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=t.device) if coded else x.new_empty((m, n))
     else:
         _cuda(out, torch.bfloat16, "out")
         if tuple(out.shape) != (m, n):
@@ -464,9 +473,9 @@ def _mx_product(w: PackedWeight, x, out, workspace, offsets):
         else:
             _check(_lib.wq_gemm_mxfp4(ctypes.byref(d), ctypes.byref(xd), _ptr(out), _stream(t)))
         return out
-    need = int(_lib.wq_gemm_mxfp4_workspace_bytes(m, k))
+    need = _mx_workspace_bytes(m, k)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=t.device)
+        workspace = x.new_empty((need + 1) // 2)
     if experts:
         _check(_lib.wq_gemm_mxfp4_experts_bf16(ctypes.byref(d), experts, _ptr(offsets), _ptr(x), m, _ptr(out),
                                                _ptr(workspace), need, _stream(t)))

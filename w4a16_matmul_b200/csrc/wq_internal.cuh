@@ -277,7 +277,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, const in
             "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
             : "=r"(done) : "r"(a), "r"(parity), "r"((uint32_t)WQ_MBAR_SUSPEND_NS) : "memory");
         if (done) return true;
-        if ((i & 7) == 0) {
+        if ((i & 63) == 63) {          // (reading the timer takes far longer than a try)
             if (abort && *(volatile const int*)abort) return false;
             const uint64_t now = global_ns();
             if (deadline == 0) deadline = now + kWaitNs;

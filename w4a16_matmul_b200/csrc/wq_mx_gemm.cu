@@ -42,8 +42,7 @@ struct Cfg {
     static constexpr int A_BYTES = BM * KB / 2, B_BYTES = BN * KB / 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;              // a multiple of 1024
     static constexpr int SC_BYTES = (BM + BN) * 16;
-    // BN = 256 fills an SM; narrower tiles leave room for two CTAs
-    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 3 : 4;
+    static constexpr int STAGES = BN == 128 ? 3 : 4;             // room for two CTAs on an SM
     static constexpr int SSTAGES = STAGES / 2 + 1;
     // tensor memory: the accumulator, then TSLOTS slots of the scale bytes of 512 columns, per
     // 128 columns CH columns: 4 for the weight rows and BN / 32, rounded up to 4, for the
@@ -54,11 +53,11 @@ struct Cfg {
     static constexpr int SLOT_COLS = 4 * CH;
     static constexpr int TSLOTS = BN <= 32 ? 3 : 4;
     static constexpr int USED_COLS = ACC_COLS + TSLOTS * SLOT_COLS;
-    static constexpr uint32_t TMEM_COLS = USED_COLS <= 128 ? 128 : USED_COLS <= 256 ? 256 : 512;
-    static_assert(USED_COLS <= 512, "tensor memory");
+    static constexpr uint32_t TMEM_COLS = USED_COLS <= 128 ? 128 : 256;
+    static_assert(USED_COLS <= 256, "tensor memory of two CTAs");
     static constexpr int BARS = 2 * STAGES + 2 * SSTAGES + 2 * TSLOTS + 1;
     static constexpr int TOTAL = STAGES * STAGE + SSTAGES * SC_BYTES + BARS * 8 + 32 + 1024;   // + alignment slack
-    static_assert(TOTAL <= 227 * 1024, "shared memory");
+    static_assert(2 * (TOTAL + 1024) <= 228 * 1024, "shared memory of two CTAs");
 };
 
 // D[128 x BN] (+)= A B^T over 64 columns: codes through descriptors, scale bytes at the
@@ -71,6 +70,21 @@ __device__ __forceinline__ void umma_mxf4(uint32_t tmem_d, uint64_t da, uint64_t
         ::"r"(tmem_d), "l"(da), "l"(db), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
 }
 
+// True in one lane of the (whole) warp. The loops of the producer and of the MMA issuer run in
+// all lanes and only issue under this predicate, which leaves their addresses and descriptors
+// uniform across the warp, as the instructions want them: issued from a loop of lane 0 alone, a
+// stage of four MMAs cost about 860 clocks of issue, whatever their size, against 512 of the
+// tensor pipe.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred q; elect.sync _|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+    return p != 0;
+}
+// mbar_wait by the whole warp, with one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, const int* abort) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(b, parity, abort));
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -80,33 +94,46 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
+// The barrier alone, for CTAs whose memory needs no order (no fence behind pending stores).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t saddr, uint32_t rank) {
     uint32_t a;
-    float v;
+    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
     return v;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 struct MxTile {
     int expert, t0, tend;            // expert (-1: none), first activation row, end of its rows
 };
 
+// Where a walk over the experts stands: those before e0 have `before` row tiles.
+struct MxScan {
+    int e0 = 0, before = 0;
+};
+
 // The row tile `mt` of all experts' tiles in order (warp-collective): expert e has
-// ceil(rows / BN) tiles. Offsets are clamped to [0, M], so no access leaves the buffers
-// whatever they hold.
-template <int BN>
-__device__ __forceinline__ MxTile find_tile(const int32_t* __restrict__ offsets, int experts, int M, int mt) {
+// ceil(rows / bn) tiles. Calls with one `at` ask for ascending mt. Offsets are clamped to
+// [0, M], so no access leaves the buffers whatever they hold.
+__device__ __forceinline__ MxTile find_tile(const int32_t* __restrict__ offsets, int experts, int M, int mt, int bn,
+                                            MxScan& at) {
     const int lane = threadIdx.x & 31;
-    int before = 0;
-    for (int e0 = 0; e0 < experts; e0 += 32) {
-        const int e = e0 + lane;
+    for (; at.e0 < experts; at.e0 += 32) {
+        const int e = at.e0 + lane;
         int lo = 0, hi = 0;
         if (e < experts) {
             lo = min(max(__ldg(offsets + e), 0), M);
             hi = min(max(__ldg(offsets + e + 1), lo), M);
         }
-        const int tiles = (hi - lo + BN - 1) / BN;
+        const int tiles = (hi - lo + bn - 1) / bn;
         int incl = tiles;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -114,20 +141,20 @@ __device__ __forceinline__ MxTile find_tile(const int32_t* __restrict__ offsets,
             if (lane >= d) incl += o;
         }
         const int total = __shfl_sync(0xFFFFFFFFu, incl, 31);
-        if (mt < before + total) {
-            const int f = __ffs(__ballot_sync(0xFFFFFFFFu, before + incl > mt)) - 1;
-            const int t0 = __shfl_sync(0xFFFFFFFFu, lo + (mt - (before + incl - tiles)) * BN, f);
+        if (mt < at.before + total) {
+            const int f = max(0, __ffs(__ballot_sync(0xFFFFFFFFu, at.before + incl > mt)) - 1);
+            const int t0 = __shfl_sync(0xFFFFFFFFu, lo + (mt - (at.before + incl - tiles)) * bn, f);
             lo = __shfl_sync(0xFFFFFFFFu, lo, f);
             hi = __shfl_sync(0xFFFFFFFFu, hi, f);
-            return MxTile{t0 >= lo && t0 < hi ? e0 + f : -1, t0, hi};
+            return MxTile{t0 >= lo && t0 < hi ? at.e0 + f : -1, t0, hi};
         }
-        before += total;
+        at.before += total;
     }
     return MxTile{-1, 0, 0};
 }
 
 template <int BN, int CL, bool EXPERTS>
-__global__ void __launch_bounds__(kThreads, BN == 256 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_ws,
                const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_xs,
                const int32_t* __restrict__ offsets, int experts, uint16_t* __restrict__ y, int M, int N, int K,
@@ -161,10 +188,14 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    if (threadIdx.x == 0) {
+        prefetch_map(&map_w); prefetch_map(&map_ws); prefetch_map(&map_x); prefetch_map(&map_xs);
+    }
     MxTile tile{0, (lin / grid_n) * BN, M};
     if (EXPERTS) {
         if (warp == 0) {
-            tile = find_tile<BN>(offsets, experts, M, lin / grid_n);
+            MxScan at;
+            tile = find_tile(offsets, experts, M, lin / grid_n, BN, at);
             if (lane == 0) { s_tile[0] = tile.expert; s_tile[1] = tile.t0; s_tile[2] = tile.tend; }
         }
         __syncthreads();
@@ -200,9 +231,10 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 
     if (warp == 0) {
         // ---------------- TMA producer ----------------
-        if (lane == 0) {
-            // the weights of the first stages: they do not depend on the kernel before this one
-            const int pre = min(nk, STAGES);
+        const bool one = elect_one();
+        // the weights of the first stages: they do not depend on the kernel before this one
+        const int pre = min(nk, STAGES);
+        if (one) {
             for (int i = 0; i < pre; ++i) {
                 if ((i & 1) == 0) {
                     mbar_expect_tx(&sfull[i >> 1], C::SC_BYTES);
@@ -217,67 +249,77 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                     tma_load_2d(stage_sc(i >> 1) + BM * 16, &map_xs, ((kt0 + i) >> 1) * 16, t0, &sfull[i >> 1]);
                 tma_load_2d(stage_b(i), &map_x, (kt0 + i) * (KB / 2), t0, &full[i]);
             }
-            int s = 0, ss = ((STAGES + 1) / 2) % SS;
-            uint32_t ph = 1, sph = (STAGES + 1) / 2 >= SS ? 1 : 0;   // parity of the stage's use
-            int i = pre;
-            for (; i < nk; ++i) {
-                if ((i & 1) == 0) {
-                    if (!mbar_wait(&sempty[ss], sph ^ 1, s_abort)) { dead(2201); break; }
+        }
+        __syncwarp();
+        int s = 0, ss = ((STAGES + 1) / 2) % SS;
+        uint32_t ph = 1, sph = (STAGES + 1) / 2 >= SS ? 1 : 0;    // parity of the stage's use
+        int i = pre, sdone = (pre + 1) / 2;                       // stages and scale stages asked for
+        for (; i < nk; ++i) {
+            if ((i & 1) == 0) {
+                if (!warp_wait(&sempty[ss], sph ^ 1, s_abort)) { dead(2201); break; }
+                if (one) {
                     mbar_expect_tx(&sfull[ss], C::SC_BYTES);
                     tma_load_2d(stage_sc(ss), &map_ws, ((kt0 + i) >> 1) * 16, w0, &sfull[ss]);
                     tma_load_2d(stage_sc(ss) + BM * 16, &map_xs, ((kt0 + i) >> 1) * 16, t0, &sfull[ss]);
-                    if (++ss == SS) { ss = 0; sph ^= 1; }
                 }
-                if (!mbar_wait(&empty[s], ph ^ 1, s_abort)) { dead(2202); break; }
+                __syncwarp();
+                ++sdone;
+                if (++ss == SS) { ss = 0; sph ^= 1; }
+            }
+            if (!warp_wait(&empty[s], ph ^ 1, s_abort)) { dead(2202); break; }
+            if (one) {
                 mbar_expect_tx(&full[s], C::STAGE);
                 tma_load_2d(stage_a(s), &map_w, (kt0 + i) * (KB / 2), w0, &full[s]);
                 tma_load_2d(stage_b(s), &map_x, (kt0 + i) * (KB / 2), t0, &full[s]);
-                if (++s == STAGES) { s = 0; ph ^= 1; }
             }
-            if (i < nk) {
-                // gave up: the copies in flight must land before the CTA may end
-                const int got_s = (i + 2) / 2;                    // scale stages asked for, at most
-                for (int j = max(0, i - STAGES); j < i; ++j) mbar_wait(&full[j % STAGES], (j / STAGES) & 1);
-                for (int j = max(0, got_s - SS); j < got_s; ++j) mbar_wait(&sfull[j % SS], (j / SS) & 1);
-            }
+            __syncwarp();
+            if (++s == STAGES) { s = 0; ph ^= 1; }
+        }
+        if (i < nk) {
+            // gave up: the copies in flight must land before the CTA may end
+            for (int j = max(0, i - STAGES); j < i; ++j) mbar_wait(&full[j % STAGES], (j / STAGES) & 1);
+            for (int j = max(0, sdone - SS); j < sdone; ++j) mbar_wait(&sfull[j % SS], (j / SS) & 1);
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
-        if (lane == 0) {
-            // E2M1 codes (format 1) in both operands, E8M0 scales, fp32 accumulator
-            constexpr uint32_t idesc0 = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | (1u << 23) |
-                                        ((uint32_t)(BM >> 4) << 24);
-            int s = 0, t = 0;
-            uint32_t ph = 0, tph = 0;
-            for (int i = 0; i < nk; ++i) {
-                if ((i & 1) == 0 && !mbar_wait(&tfull[t], tph, s_abort)) { dead(2203); break; }
-                if (!mbar_wait(&full[s], ph, s_abort)) { dead(2204); break; }
-                asm volatile("tcgen05.fence::after_thread_sync;");
-                const uint64_t da = sw128_desc(smem_u32(stage_a(s))), db = sw128_desc(smem_u32(stage_b(s)));
-                const uint32_t sf = tmem + (uint32_t)(C::ACC_COLS + t * C::SLOT_COLS + (i & 1) * 2 * C::CH);
-                const int left = (K - (kt0 + i) * KB) / 64;       // K is a multiple of 64
+        // E2M1 codes (format 1) in both operands, E8M0 scales, fp32 accumulator
+        constexpr uint32_t idesc0 = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | (1u << 23) |
+                                    ((uint32_t)(BM >> 4) << 24);
+        const bool one = elect_one();
+        int s = 0, t = 0;
+        uint32_t ph = 0, tph = 0;
+        for (int i = 0; i < nk; ++i) {
+            if ((i & 1) == 0 && !warp_wait(&tfull[t], tph, s_abort)) { dead(2203); break; }
+            if (!warp_wait(&full[s], ph, s_abort)) { dead(2204); break; }
+            asm volatile("tcgen05.fence::after_thread_sync;");
+            const uint64_t da = sw128_desc(smem_u32(stage_a(s))), db = sw128_desc(smem_u32(stage_b(s)));
+            const uint32_t sf = tmem + (uint32_t)(C::ACC_COLS + t * C::SLOT_COLS + (i & 1) * 2 * C::CH);
+            const int left = (K - (kt0 + i) * KB) / 64;           // K is a multiple of 64
+            // 64 codes are 32 bytes of the swizzle row: + 2 in descriptor units; bytes 0-1 or 2-3 of
+            // the scale words
+            auto mma = [&](int j) {
+                const uint32_t id = (uint32_t)(j & 1) * 2u, sfa = sf + (uint32_t)((j >> 1) * C::CH);
+                umma_mxf4(tmem, da + 2 * j, db + 2 * j, idesc0 | id << 4 | id << 29, sfa, sfa + 4,
+                          (i > 0 || j > 0) ? 1u : 0u);
+            };
+            if (one) {
+                if (left >= 4) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j < left) {
-                        // 64 codes are 32 bytes of the swizzle row: + 2 in descriptor units; bytes
-                        // 0-1 or 2-3 of the scale words
-                        const uint32_t id = (uint32_t)(j & 1) * 2u;
-                        const uint32_t sfa = sf + (uint32_t)((j >> 1) * C::CH);
-                        umma_mxf4(tmem, da + 2 * j, db + 2 * j, idesc0 | id << 4 | id << 29, sfa, sfa + 4,
-                                  (i > 0 || j > 0) ? 1u : 0u);
-                    }
+                    for (int j = 0; j < 4; ++j) mma(j);
+                } else {
+                    for (int j = 0; j < left; ++j) mma(j);
                 }
                 umma_commit(&empty[s]);                           // fire once these MMAs are done
-                if (++s == STAGES) { s = 0; ph ^= 1; }
-                if ((i & 1) || i + 1 == nk) {
-                    umma_commit(&tfree[t]);
-                    if (++t == TS) { t = 0; tph ^= 1; }
-                }
+                if ((i & 1) || i + 1 == nk) umma_commit(&tfree[t]);
             }
-            // a commit also after giving up: it fires once every MMA issued so far is done, so
-            // tensor memory is never freed under a running MMA
-            umma_commit(acc_full);
+            __syncwarp();
+            if (++s == STAGES) { s = 0; ph ^= 1; }
+            if ((i & 1) && ++t == TS) { t = 0; tph ^= 1; }
         }
+        // a commit also after giving up: it fires once every MMA issued so far is done, so tensor
+        // memory is never freed under a running MMA
+        if (one) umma_commit(acc_full);
+        __syncwarp();
     } else {
         // ---------------- scale bytes into tensor memory, then the epilogue ----------------
         const int q = warp & 3;                                   // this warp's lane quarter
@@ -301,8 +343,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                 v[j] = r.x; v[C::CH + j] = r.y; v[2 * C::CH + j] = r.z; v[3 * C::CH + j] = r.w;
             }
             const uint32_t dst = lane_base + (uint32_t)(C::ACC_COLS + t * C::SLOT_COLS);
-            tmem_st_part<32>(dst, v);
-            if constexpr (C::SLOT_COLS == 48) tmem_st_part<16>(dst + 32, v + 32);
+            tmem_st_part<C::SLOT_COLS>(dst, v);
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
@@ -338,21 +379,353 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     if (CL > 1) {
         cluster_sync();                                           // every rank's partial sums are in place
         if (warp >= 2) {
-            const int i = (int)threadIdx.x - 64, n = n0 + i;
-            if (n < N)
-                for (int c = crank; c < BN && t0 + c < tend; c += CL) {
-                    float sum = 0.f;
+            // rank r adds the activation rows r, r + CL, ...: one of them a warp, 4 weight rows a lane
+            const int n = n0 + 4 * lane;
+            const uint32_t base = smem_u32(smem) + 16u * (uint32_t)lane;
+#pragma unroll 2
+            for (int c = crank + CL * (warp - 2); c < BN; c += 4 * CL) {
+                if (t0 + c >= tend) break;
+                float4 v[CL];
 #pragma unroll
-                    for (int r = 0; r < CL; ++r) sum += ld_cluster_f32(smem_u32(smem) + (uint32_t)(c * BM + i) * 4, r);
-                    y[(size_t)(t0 + c) * N + n] = (uint16_t)float_to_bf16_bits(sum);
+                for (int r = 0; r < CL; ++r) v[r] = ld_cluster_v4(base + (uint32_t)(c * BM * 4), r);
+                float4 sum = v[0];
+#pragma unroll
+                for (int r = 1; r < CL; ++r) { sum.x += v[r].x; sum.y += v[r].y; sum.z += v[r].z; sum.w += v[r].w; }
+                uint16_t* yr = y + (size_t)(t0 + c) * N;
+                const uint2 o = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+                if ((N & 3) == 0) {
+                    if (n < N) *(uint2*)(yr + n) = o;
+                } else {
+                    if (n < N) yr[n] = (uint16_t)o.x;
+                    if (n + 1 < N) yr[n + 1] = (uint16_t)(o.x >> 16);
+                    if (n + 2 < N) yr[n + 2] = (uint16_t)o.y;
+                    if (n + 3 < N) yr[n + 3] = (uint16_t)(o.y >> 16);
                 }
+            }
         }
-        cluster_sync();                                           // ... and read
+        __syncwarp();
+        cluster_sync_relaxed();                                   // ... and read
     }
     __syncthreads();
     if (warp == 1) {
         asm volatile("tcgen05.fence::after_thread_sync;");
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// Many activation rows: pairs of CTAs (cta_group::2) on tiles of 256 weight rows x bn <= 256
+// activation rows, walked by a persistent grid. Each CTA of a pair holds half of the weight
+// rows and half of the activation rows in shared memory and accumulates its 128 weight rows x
+// bn: per MMA it reads 128 + bn / 2 rows where a single CTA reads 128 + bn. Shared memory is
+// what bounds the 4-bit product: at 128 x 256 the MMA's reads and the TMA's writes are 192
+// bytes a clock against 128 (measured 834 clocks a stage of 256 columns; the MMAs take 512).
+//   warp 0      TMA producer of its CTA (both signal the leader's barrier);
+//   warp 1      MMA issuer (the leader's CTA only), commits to both CTAs;
+//   warps 2-5   scale bytes into tensor memory: the CTA's 128 weight rows and all activation rows;
+//   warps 6-13  epilogue: the accumulator into registers as bf16, which frees it for the next
+//               tile, then transposed through shared memory into 16-byte stores.
+// ---------------------------------------------------------------------------------------
+struct Pair {
+    static constexpr int THREADS = 448;
+    static constexpr int STAGES = 5, SS = 3, TS = 4;
+    static constexpr int A_BYTES = BM * KB / 2, B_BYTES = 128 * KB / 2, STAGE = A_BYTES + B_BYTES;
+    static constexpr int SC_BYTES = (BM + 256) * 16;
+    static constexpr int CH = 12, SLOT_COLS = 4 * CH, ACC_COLS = 256;
+    static constexpr int EPI_WARP = 2048;                        // 32 tokens x 32 weight rows of bf16
+    static constexpr int BARS = 2 * STAGES + 2 * SS + 2 * TS + 2;
+    static constexpr int TOTAL = STAGES * STAGE + SS * SC_BYTES + 8 * EPI_WARP + BARS * 8 + 16 + 1024;
+    static_assert(ACC_COLS + TS * SLOT_COLS <= 512, "tensor memory");
+    static_assert(TOTAL <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    return a;
+}
+// (A release at cluster scope would stand here too, and cost a fence a time: measured 0.17 us a
+// stage. What crosses CTAs is ordered by the tcgen05 fences around the arrival.)
+__device__ __forceinline__ void mbar_arrive_leader(const uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(b)) : "memory");
+}
+// A tile into this CTA's shared memory, its bytes counted on the leader's barrier `bar`.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t sfa,
+                                               uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p; }"
+        ::"r"(tmem_d), "l"(da), "l"(db), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+}
+
+template <bool EXPERTS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
+mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_ws,
+                    const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_xs,
+                    const int32_t* __restrict__ offsets, int experts, uint16_t* __restrict__ y, int M, int N, int K,
+                    int grid_n, int grid_m, int bn) {
+    using C = Pair;
+    constexpr int STAGES = C::STAGES, SS = C::SS, TS = C::TS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* sc_smem = smem + STAGES * C::STAGE;
+    uint8_t* epi_smem = sc_smem + SS * C::SC_BYTES;
+    uint64_t* full = (uint64_t*)(epi_smem + 8 * C::EPI_WARP);   // (leader's) codes of both CTAs' stage landed
+    uint64_t* empty = full + STAGES;                             // stage read by its MMAs
+    uint64_t* sfull = empty + STAGES;                            // scale bytes of 512 columns landed
+    uint64_t* sempty = sfull + SS;                               // ... and read by the movers
+    uint64_t* tfull = sempty + SS;                               // (leader's) both CTAs' scales in tensor memory
+    uint64_t* tfree = tfull + TS;                                // ... and read by their MMAs
+    uint64_t* acc_full = tfree + TS;
+    uint64_t* acc_free = acc_full + 1;                           // (leader's) both accumulators read
+    uint32_t* s_tmem = (uint32_t*)(acc_free + 1);
+    int* s_abort = (int*)(s_tmem + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+        for (int s = 0; s < SS; ++s) { mbar_init(&sfull[s], 1); mbar_init(&sempty[s], 4); }
+        for (int s = 0; s < TS; ++s) { mbar_init(&tfull[s], 8); mbar_init(&tfree[s], 1); }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_free, 16);
+        *s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (threadIdx.x == 0) {
+        prefetch_map(&map_w); prefetch_map(&map_ws); prefetch_map(&map_x); prefetch_map(&map_xs);
+    }
+    __syncwarp();
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_tmem)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        asm volatile("tcgen05.fence::before_thread_sync;");
+    }
+    __syncthreads();
+    cluster_sync_relaxed();                                      // the peer's barriers are ready too
+    asm volatile("tcgen05.fence::after_thread_sync;");
+    const uint32_t tmem = *s_tmem;
+    const int nk = (K + KB - 1) / KB, nsk = (nk + 1) / 2;        // stages and scale stages of a tile
+    const int step = (int)gridDim.x / 2;
+
+    auto stage_a = [&](int s) { return smem + s * C::STAGE; };
+    auto stage_b = [&](int s) { return smem + s * C::STAGE + C::A_BYTES; };
+    auto stage_sc = [&](int s) { return sc_smem + s * C::SC_BYTES; };
+    auto dead = [&](int code) {
+        *(volatile int*)s_abort = 1;
+        atomicCAS(&g_mx_error, 0, code);
+    };
+    MxScan at;
+    // tile number `lin`: its weight-row tile nt (fastest) and its activation rows; false: none
+    auto get = [&](int lin, int& n0, MxTile& t) {
+        n0 = (lin % grid_n) * 256 + rank * BM;
+        const int mt = lin / grid_n;
+        if (EXPERTS) {
+            t = find_tile(offsets, experts, M, mt, bn, at);
+            return t.expert >= 0;
+        }
+        t = MxTile{0, mt * bn, M};
+        return mt < grid_m;
+    };
+    const uint32_t sc_bytes = (uint32_t)(BM + bn) * 16, b_bytes = (uint32_t)(bn / 2) * (KB / 2);
+
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        int s = 0, ss = 0, done = 0, sdone = 0;                  // stages and scale stages asked for
+        uint32_t ph = 0, sph = 0;
+        bool ok = true;
+        int n0;
+        MxTile t;
+        const bool one = elect_one();
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        for (int lin = (int)blockIdx.x / 2; ok && get(lin, n0, t); lin += step) {
+            const int w0 = t.expert * N + n0;
+            for (int i = 0; i < nk; ++i) {
+                if ((i & 1) == 0) {
+                    if (!warp_wait(&sempty[ss], sph ^ 1, s_abort)) { dead(2211); ok = false; break; }
+                    if (one) {
+                        mbar_expect_tx(&sfull[ss], sc_bytes);
+                        tma_load_2d(stage_sc(ss), &map_ws, (i >> 1) * 16, w0, &sfull[ss]);
+                        tma_load_2d(stage_sc(ss) + BM * 16, &map_xs, (i >> 1) * 16, t.t0, &sfull[ss]);
+                    }
+                    __syncwarp();
+                    ++sdone;
+                    if (++ss == SS) { ss = 0; sph ^= 1; }
+                }
+                if (!warp_wait(&empty[s], ph ^ 1, s_abort)) { dead(2212); ok = false; break; }
+                if (one) {
+                    if (rank == 0) mbar_expect_tx(&full[s], 2 * (C::A_BYTES + b_bytes));
+                    const uint32_t bar = leader_addr(&full[s]);
+                    tma_load_pair(stage_a(s), &map_w, i * (KB / 2), w0, bar);
+                    tma_load_pair(stage_b(s), &map_x, i * (KB / 2), t.t0 + rank * (bn / 2), bar);
+                }
+                __syncwarp();
+                ++done;
+                if (++s == STAGES) { s = 0; ph ^= 1; }
+            }
+        }
+        if (!ok) {
+            // gave up: the copies in flight must land before the CTAs may end
+            if (rank == 0)
+                for (int j = max(0, done - STAGES); j < done; ++j) mbar_wait(&full[j % STAGES], (j / STAGES) & 1);
+            for (int j = max(0, sdone - SS); j < sdone; ++j) mbar_wait(&sfull[j % SS], (j / SS) & 1);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (leader) ----------------
+        if (rank == 0) {
+            const uint32_t idesc0 = (1u << 7) | (1u << 10) | ((uint32_t)(bn >> 3) << 17) | (1u << 23) |
+                                    ((uint32_t)(256 >> 4) << 24);
+            int s = 0, ts = 0;
+            uint32_t ph = 0, tph = 0, aph = 1;
+            bool ok = true;
+            int n0;
+            MxTile t;
+            const bool one = elect_one();
+            for (int lin = (int)blockIdx.x / 2; ok && get(lin, n0, t); lin += step) {
+                if (!warp_wait(acc_free, aph, s_abort)) { dead(2213); ok = false; }
+                for (int i = 0; ok && i < nk; ++i) {
+                    if ((i & 1) == 0 && !warp_wait(&tfull[ts], tph, s_abort)) { dead(2214); ok = false; break; }
+                    if (!warp_wait(&full[s], ph, s_abort)) { dead(2215); ok = false; break; }
+                    asm volatile("tcgen05.fence::after_thread_sync;");
+                    const uint64_t da = sw128_desc(smem_u32(stage_a(s))), db = sw128_desc(smem_u32(stage_b(s)));
+                    const uint32_t sf = tmem + (uint32_t)(C::ACC_COLS + ts * C::SLOT_COLS + (i & 1) * 2 * C::CH);
+                    const int left = (K - i * KB) / 64;
+                    auto mma = [&](int j) {
+                        const uint32_t id = (uint32_t)(j & 1) * 2u, sfa = sf + (uint32_t)((j >> 1) * C::CH);
+                        umma_mxf4_pair(tmem, da + 2 * j, db + 2 * j, idesc0 | id << 4 | id << 29, sfa, sfa + 4,
+                                       (i > 0 || j > 0) ? 1u : 0u);
+                    };
+                    if (one) {
+                        if (left >= 4) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) mma(j);
+                        } else {
+                            for (int j = 0; j < left; ++j) mma(j);
+                        }
+                        umma_commit_pair(&empty[s]);
+                        if ((i & 1) || i + 1 == nk) umma_commit_pair(&tfree[ts]);
+                    }
+                    __syncwarp();
+                    if (++s == STAGES) { s = 0; ph ^= 1; }
+                    if (((i & 1) || i + 1 == nk) && ++ts == TS) { ts = 0; tph ^= 1; }
+                }
+                // (also after giving up, and then waited for: tensor memory is not freed under a
+                // running MMA)
+                if (one) umma_commit_pair(acc_full);
+                __syncwarp();
+                if (!ok) mbar_wait(acc_full, aph ^ 1);
+                aph ^= 1;
+            }
+        }
+    } else if (warp < 6) {
+        // ---------------- scale bytes into tensor memory ----------------
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        int ss = 0, ts = 0, n0;
+        uint32_t sph = 0, tph = 1;
+        bool ok = true;
+        MxTile t;
+        for (int lin = (int)blockIdx.x / 2; ok && get(lin, n0, t); lin += step) {
+            for (int it = 0; it < nsk; ++it) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sfull[ss], sph, s_abort) && mbar_wait(&tfree[ts], tph, s_abort));
+                if (!ok) { dead(2216); break; }
+                const uint4* sc = (const uint4*)stage_sc(ss);
+                uint32_t v[C::SLOT_COLS];
+#pragma unroll
+                for (int j = 0; j < C::CH; ++j) {                 // (rows past bn: columns that no MMA reads)
+                    const uint4 r = sc[32 * j + lane];
+                    v[j] = r.x; v[C::CH + j] = r.y; v[2 * C::CH + j] = r.z; v[3 * C::CH + j] = r.w;
+                }
+                const uint32_t dst = lane_base + (uint32_t)(C::ACC_COLS + ts * C::SLOT_COLS);
+                tmem_st_part<32>(dst, v);
+                tmem_st_part<16>(dst + 32, v + 32);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) { mbar_arrive(&sempty[ss]); mbar_arrive_leader(&tfull[ts]); }
+                if (++ss == SS) { ss = 0; sph ^= 1; }
+                if (++ts == TS) { ts = 0; tph ^= 1; }
+            }
+        }
+    } else {
+        // ---------------- epilogue ----------------
+        const int q = warp & 3, h = (warp - 6) >> 2;              // lane quarter; columns 128 h .. 128 h + 127
+        const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(128 * h);
+        uint8_t* buf = epi_smem + (warp - 6) * C::EPI_WARP;
+        const bool wide = (N & 7) == 0;                           // rows of y are then 16-byte aligned
+        uint32_t aph = 0;
+        bool ok = true;
+        int n0;
+        MxTile t;
+        for (int lin = (int)blockIdx.x / 2; ok && get(lin, n0, t); lin += step, aph ^= 1) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, aph, s_abort)) &&
+                 !__any_sync(0xFFFFFFFFu, *(volatile int*)s_abort != 0);
+            if (!ok) { dead(2217); break; }
+            asm volatile("tcgen05.fence::after_thread_sync;");
+            // activation rows of this tile that this warp holds
+            const int rows = min(min(bn - 128 * h, 128), t.tend - t.t0 - 128 * h);
+            uint32_t p[64];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (32 * c < rows) {
+                    uint32_t v[32];
+                    tmem_ld32(src + 32u * (uint32_t)c, v);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        p[16 * c + j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive_leader(acc_free);
+            const int nq = n0 + 32 * q;                           // this warp's first weight row
+            uint16_t* yt = y + (size_t)(t.t0 + 128 * h) * N;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (32 * c >= rows) break;
+                if (wide) {
+                    // two lanes swap halves, so that each holds two neighbouring weight rows of one
+                    // activation row; then 32 activation rows of 64 bytes
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const uint32_t own = p[16 * c + j], other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+                        const uint32_t two = (lane & 1) ? prmt(other, own, 0x7632u) : prmt(own, other, 0x5410u);
+                        *(uint32_t*)(buf + (2 * j + (lane & 1)) * 64 + (lane >> 1) * 4) = two;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 32 * c + 8 * r + (lane >> 2), n = nq + 8 * (lane & 3);
+                        const uint4 o = *(const uint4*)(buf + (8 * r + (lane >> 2)) * 64 + (lane & 3) * 16);
+                        if (row < rows && n < N) *(uint4*)(yt + (size_t)row * N + n) = o;
+                    }
+                    __syncwarp();
+                } else if (nq + lane < N) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const uint32_t two = p[16 * c + j / 2];
+                        if (32 * c + j < rows) yt[(size_t)(32 * c + j) * N + nq + lane] = (uint16_t)(j & 1 ? two >> 16 : two);
+                    }
+                }
+            }
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;");
+    __syncwarp();
+    cluster_sync_relaxed();                                      // no signal is under way to either CTA
+    if (warp == 1) {
+        asm volatile("tcgen05.fence::after_thread_sync;");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
 }
 
@@ -413,6 +786,28 @@ wq_status launch_one(const Maps& mp, const int32_t* offsets, int experts, uint16
     return check_launch("mxfp4 gemm");
 }
 
+template <bool EXPERTS>
+wq_status launch_pair(const Maps& mp, const int32_t* offsets, int experts, uint16_t* y, int M, int N, int K,
+                      int grid_n, int grid_m, int bn, bool overlap, cudaStream_t s) {
+    auto k = mx_gemm_pair_kernel<EXPERTS>;
+    static bool raised = false;
+    if (!raised && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Pair::TOTAL) == cudaSuccess)
+        raised = true;
+    cudaLaunchConfig_t cfg = {};
+    const int64_t tiles = (int64_t)grid_n * grid_m;
+    cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, sm_count() / 2)), 1, 1);
+    cfg.blockDim = dim3(Pair::THREADS);
+    cfg.dynamicSmemBytes = Pair::TOTAL;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    cudaLaunchKernelEx(&cfg, k, mp.w, mp.ws, mp.x, mp.xs, offsets, experts, y, M, N, K, grid_n, grid_m, bn);
+    return check_launch("mxfp4 gemm (pairs)");
+}
+
 }  // namespace
 
 wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t* xp, const uint8_t* xsc, int64_t m,
@@ -424,19 +819,40 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
     const int sms = sm_count();
     // activation rows a tile should hold: all of them, or the rows of a typical expert
     const int64_t rows = offsets ? (m + experts - 1) / experts : m;
-    const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
-    // row tiles: with experts the most that any distribution of the rows needs
-    const int64_t grid_m = offsets ? m / bn + std::min<int64_t>(experts, m) : (m + bn - 1) / bn;
-    if (grid_m * grid_n > 0x7FFFFFFF) return fail(WQ_EUNSUPPORTED, "more than 2^31 - 1 tiles");
-    // K split over a cluster while the tiles leave SMs idle and every rank keeps 512 columns
-    int cl = 1;
-    if (!offsets && bn <= 64)
-        while (cl < 8 && grid_m * grid_n * cl * 2 <= 2 * (int64_t)sms && KT / (cl * 2) >= 2) cl *= 2;
-    int per = (KT + cl - 1) / cl;
-    per += per & 1;
     Maps mp;
     const int64_t pitch = mx_pitch(k);
     wq_status st;
+    if (rows > 128) {
+        const int gn = (N + 255) / 256;
+        // as few activation tiles as hold all rows, of equal width: a stage of 256 columns takes 617
+        // clocks at 256 rows and still 505 at 64 (16384 columns, per pair)
+        const int64_t wide = (m + 255) / 256;
+        const int bn = offsets ? 256 : (int)((m + 16 * wide - 1) / (16 * wide)) * 16;
+        const int64_t gm = offsets ? m / bn + std::min<int64_t>(experts, m) : (m + bn - 1) / bn;
+        if (gm * gn > 0x3FFFFFFF) return fail(WQ_EUNSUPPORTED, "more than 2^30 - 1 tiles");
+        if ((st = encode_u8(&mp.w, wp, k / 2, n * experts, KB / 2, BM, true, "the weight codes"))) return st;
+        if ((st = encode_u8(&mp.ws, wsc, pitch, n * experts, 16, BM, false, "the weight scales"))) return st;
+        if ((st = encode_u8(&mp.x, xp, k / 2, m, KB / 2, bn / 2, true, "the activation codes"))) return st;
+        if ((st = encode_u8(&mp.xs, xsc, pitch, m, 16, bn, false, "the activation scales"))) return st;
+        return offsets ? launch_pair<true>(mp, offsets, experts, y, M, N, K, gn, (int)gm, bn, overlap, s)
+                       : launch_pair<false>(mp, offsets, experts, y, M, N, K, gn, (int)gm, bn, overlap, s);
+    }
+    const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    // row tiles: with experts the most that any distribution of the rows needs
+    const int64_t grid_m = offsets ? m / bn + std::min<int64_t>(experts, m) : (m + bn - 1) / bn;
+    if (grid_m * grid_n > 0x7FFFFFFF) return fail(WQ_EUNSUPPORTED, "more than 2^31 - 1 tiles");
+    // K split over a cluster: one CTA an SM as long as each keeps 512 columns, two while each
+    // keeps 1024 (4096 x 4096 at one row, 32 tiles: 9.0 / 6.8 / 6.0 / 6.7 us at 1 / 2 / 4 / 8 ranks)
+    int cl = 1;
+    if (!offsets)
+        while (cl < 8) {
+            const int64_t ctas = grid_m * grid_n * cl * 2;
+            const int stages = KT / (cl * 2);
+            if (!((ctas <= sms && stages >= 2) || (ctas <= 2 * (int64_t)sms && stages >= 4))) break;
+            cl *= 2;
+        }
+    int per = (KT + cl - 1) / cl;
+    per += per & 1;
     if ((st = encode_u8(&mp.w, wp, k / 2, n * experts, KB / 2, BM, true, "the weight codes"))) return st;
     if ((st = encode_u8(&mp.ws, wsc, pitch, n * experts, 16, BM, false, "the weight scales"))) return st;
     if ((st = encode_u8(&mp.x, xp, k / 2, m, KB / 2, bn, true, "the activation codes"))) return st;
@@ -450,8 +866,7 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
         case 16: return WQ_MX_CL(16);
         case 32: return WQ_MX_CL(32);
         case 64: return WQ_MX_CL(64);
-        case 128: return offsets ? WQ_MX(128, 1, true) : WQ_MX(128, 1, false);
-        default: return offsets ? WQ_MX(256, 1, true) : WQ_MX(256, 1, false);
+        default: return WQ_MX_CL(128);
     }
 #undef WQ_MX_CL
 #undef WQ_MX
