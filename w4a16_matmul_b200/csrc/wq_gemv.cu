@@ -113,6 +113,28 @@ __device__ __forceinline__ void dyadic_pairs_scaled(uint32_t w, uint32_t c1, uin
     p[3] = bf16x2_fma(t & 0x00F000F0u, c2, d);
 }
 
+// MXFP4 levels of the 8 codes of one packed word, pair j = (code j, code j + 4) as for dyadic.
+// A code's bits s ee m, put at bit 15 and bits 8..6 of a bf16, are its level times 2^-126 (the
+// format's subnormal 1/2 included): one masked nibble pair times 2^12 + 2^6 holds both, and the
+// group's factor 2^(s - 1) below makes up for 2^-126. 9 logic operations a word where the table
+// lookup takes 16; the integer and bf16x2 multiplies run on the other pipe.
+__device__ __forceinline__ void mx4_pairs_fast(uint32_t w, uint32_t (&p)[4]) {
+    const uint32_t t = w >> 8;
+    p[0] = ((w & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+    p[1] = ((w & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
+    p[2] = ((t & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+    p[3] = ((t & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
+}
+// The same pairs of levels themselves, from the table.
+__device__ __forceinline__ void mx4_pairs(uint32_t w, uint32_t (&p)[4]) {
+    uint32_t n[4];
+    mx4_word(w, n);
+    p[0] = prmt(n[0], n[2], 0x5410u);
+    p[1] = prmt(n[0], n[2], 0x7632u);
+    p[2] = prmt(n[1], n[3], 0x5410u);
+    p[3] = prmt(n[1], n[3], 0x7632u);
+}
+
 enum Kind { kDyadic64 = 0, kDyadic32 = 1, kLut16 = 2, kLloyd8 = 3, kMx4 = 4 };
 
 // Per-lane state of one 256-column step for R 16-row blocks: the 32 bytes of rows g and
@@ -253,7 +275,9 @@ __device__ __forceinline__ void load_step_full(Step<KIND, R>& st, const LaneRows
 // pair. xs0 / xs1: this lane's 16-byte slot of the step in the staged rows of batch
 // columns g and g + 8 (lanes of unused batch columns read some staged row; their outputs
 // are never stored).
-template <int KIND, int NB, int R>
+// MXFP4: MXFAST where every scale byte of the step is at most 128 (scales up to 2), so that 2^(s -
+// 1) is a bf16 number.
+template <int KIND, int NB, int R, bool MXFAST = true>
 __device__ __forceinline__ void compute_step_staged(const Step<KIND, R>& st, float (&acc)[R][NB][4],
                                                     const uint8_t* xs0, const uint8_t* xs1) {
     constexpr int J = (KIND == kDyadic32) ? 2 : 1;
@@ -280,8 +304,9 @@ __device__ __forceinline__ void compute_step_staged(const Step<KIND, R>& st, flo
                     phi[r][h][2 * j + 1] = prmt(b45, b67, 0x7531u);
                 }
             } else if (KIND == kMx4) {
-                ms[r][h][0] = mx_scale_pair(st.aux[r][h][0] & 0xFFu);
-                ms[r][h][1] = mx_scale_pair(st.aux[r][h][0] >> 8);
+                const uint32_t s0 = st.aux[r][h][0] & 0xFFu, s1 = st.aux[r][h][0] >> 8;
+                ms[r][h][0] = MXFAST ? ((s0 + 126) << 7) * 0x10001u : mx_scale_pair(s0);
+                ms[r][h][1] = MXFAST ? ((s1 + 126) << 7) * 0x10001u : mx_scale_pair(s1);
             } else if (KIND == kLut16) {
                 const uint32_t* L = st.aux[r][h];
 #pragma unroll
@@ -320,8 +345,13 @@ __device__ __forceinline__ void compute_step_staged(const Step<KIND, R>& st, flo
                     mma_bf16_16816(acc[r][nb], q0[2], q1[2], q0[3], q1[3], b[nb][2], b[nb][3]);
                 }
             } else if (KIND == kMx4) {
-                mx4_word(st.w[r][0][sub], q0);
-                mx4_word(st.w[r][1][sub], q1);
+                if (MXFAST) {
+                    mx4_pairs_fast(st.w[r][0][sub], q0);
+                    mx4_pairs_fast(st.w[r][1][sub], q1);
+                } else {
+                    mx4_pairs(st.w[r][0][sub], q0);
+                    mx4_pairs(st.w[r][1][sub], q1);
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {           // exact: a level times a power of two
                     q0[j] = bf16x2_fma(q0[j], ms[r][0][sub >> 2], 0x80008000u);
@@ -406,12 +436,19 @@ __device__ __forceinline__ void compute_step_exact(const GemvProblem& pb, int ro
     }
 }
 
-// True when every scale of the step lies in [2^-59, 2^62) (biased exponent 68..188), the
-// range the one-FMA reconstruction covers.
+// True when every scale of the step lies in the range the fast reconstruction covers: dyadic
+// [2^-59, 2^62) (biased exponent 68..188), MXFP4 bytes up to 128.
 template <int KIND, int R>
 __device__ __forceinline__ bool step_scales_in_range(const Step<KIND, R>& st) {
-    if (KIND == kLut16 || KIND == kLloyd8 || KIND == kMx4) return true;
+    if (KIND == kLut16 || KIND == kLloyd8) return true;
     bool ok = true;
+    if (KIND == kMx4) {                                 // no scale byte above 128
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) ok = ok && (st.aux[r][h][0] & 0xFFu) <= 128 && (st.aux[r][h][0] >> 8) <= 128;
+        return ok;
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -431,8 +468,8 @@ __device__ __forceinline__ bool step_scales_in_range(const Step<KIND, R>& st) {
 // columns paired (0,4), (1,5), (2,6), (3,7); LUT16: fp16 in natural order, each batch row's
 // 256 columns of a step times the power of two 2^e that puts their largest magnitude in
 // [2^15, 2^16) (lut_x_exponent), with 2^-e in xf[b * ns + step] for the step's sums (a warp
-// stages exactly one row's step: its 32 consecutive 8-column blocks); LLOYD8S and MXFP4:
-// bf16 in natural order. Columns at or beyond K are zero. Stages steps [c0, c0 + ns) of all B rows
+// stages exactly one row's step: its 32 consecutive 8-column blocks); MXFP4: bf16, paired
+// as for dyadic; LLOYD8S: bf16 in natural order. Columns at or beyond K are zero. Stages steps [c0, c0 + ns) of all B rows
 // with the whole CTA; returns (dyadic) whether some staged |x| reaches 2^64 or is not finite.
 template <int KIND, int THREADS>
 __device__ __forceinline__ bool stage_x(uint8_t* xs, const uint16_t* x, int B, int K, int c0,
@@ -473,7 +510,10 @@ __device__ __forceinline__ bool stage_x(uint8_t* xs, const uint16_t* x, int B, i
                     f.x = bf16x2_to_f16x2_scaled(v[u].x, s1, s2); f.y = bf16x2_to_f16x2_scaled(v[u].y, s1, s2);
                     f.z = bf16x2_to_f16x2_scaled(v[u].z, s1, s2); f.w = bf16x2_to_f16x2_scaled(v[u].w, s1, s2);
                 }
-            } else if (KIND == kLloyd8 || KIND == kMx4) {
+            } else if (KIND == kMx4) {                  // bf16, columns paired as for dyadic
+                f.x = prmt(v[u].x, v[u].z, 0x5410u); f.y = prmt(v[u].x, v[u].z, 0x7632u);
+                f.z = prmt(v[u].y, v[u].w, 0x5410u); f.w = prmt(v[u].y, v[u].w, 0x7632u);
+            } else if (KIND == kLloyd8) {
                 f = v[u];                               // bf16 in natural order
             } else {
                 // a half of magnitude bits m >= 0x5F80 (|x| >= 2^64, inf, NaN) carries into
@@ -632,7 +672,12 @@ gemv_kernel(const __grid_constant__ GemvParams<MAXP> prm) {
 #pragma unroll
                         for (int j = h; j < 4; j += 2) acc[r][nb][j] = fmaf(sacc[r][nb][j], f, acc[r][nb][j]);
                 }
-        } else if (KIND == kLloyd8 || KIND == kMx4 || (!xbad && __all_sync(0xFFFFFFFFu, step_scales_in_range<KIND, R>(st)))) {
+        } else if constexpr (KIND == kMx4) {
+            if (__all_sync(0xFFFFFFFFu, step_scales_in_range<KIND, R>(st)))
+                compute_step_staged<KIND, NB, R, true>(st, acc, xs0 + 512 * (s - c0), xs1 + 512 * (s - c0));
+            else
+                compute_step_staged<KIND, NB, R, false>(st, acc, xs0 + 512 * (s - c0), xs1 + 512 * (s - c0));
+        } else if (KIND == kLloyd8 || (!xbad && __all_sync(0xFFFFFFFFu, step_scales_in_range<KIND, R>(st)))) {
             compute_step_staged<KIND, NB, R>(st, acc, xs0 + 512 * (s - c0), xs1 + 512 * (s - c0));
         } else {
             compute_step_exact<KIND, NB, R>(pb, row0, g, s * 256 + t * 64, N, K, B, acc);

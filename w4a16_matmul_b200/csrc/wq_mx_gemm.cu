@@ -70,21 +70,6 @@ __device__ __forceinline__ void umma_mxf4(uint32_t tmem_d, uint64_t da, uint64_t
         ::"r"(tmem_d), "l"(da), "l"(db), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
 }
 
-// True in one lane of the (whole) warp. The loops of the producer and of the MMA issuer run in
-// all lanes and only issue under this predicate, which leaves their addresses and descriptors
-// uniform across the warp, as the instructions want them: issued from a loop of lane 0 alone, a
-// stage of four MMAs cost about 860 clocks of issue, whatever their size, against 512 of the
-// tensor pipe.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{ .reg .pred q; elect.sync _|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q; }" : "=r"(p));
-    return p != 0;
-}
-// mbar_wait by the whole warp, with one answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, const int* abort) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(b, parity, abort));
-}
-
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

@@ -12,6 +12,21 @@ namespace wq {
 // cuTensorMapEncodeTiled of the driver, or nullptr (wq_gemm.cu).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
+// True in one lane of the (whole) warp. The loops of the producer and of the MMA issuer run in
+// all lanes and only issue under this predicate, which leaves their addresses and descriptors
+// uniform across the warp, as the instructions want them: issued from a loop of lane 0 alone, a
+// stage of four MMAs cost about 860 clocks of issue, whatever their size, against 512 of the
+// tensor pipe.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred q; elect.sync _|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+    return p != 0;
+}
+// mbar_wait by the whole warp, with one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, const int* abort) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(b, parity, abort));
+}
+
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
