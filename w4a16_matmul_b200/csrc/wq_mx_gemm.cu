@@ -405,21 +405,27 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 // bn: per MMA it reads 128 + bn / 2 rows where a single CTA reads 128 + bn. Shared memory is
 // what bounds the 4-bit product: at 128 x 256 the MMA's reads and the TMA's writes are 192
 // bytes a clock against 128 (measured 834 clocks a stage of 256 columns; the MMAs take 512).
-//   warp 0      TMA producer of its CTA (both signal the leader's barrier);
+//   warp 0      TMA producer of its CTA's codes (both CTAs signal the leader's barrier);
 //   warp 1      MMA issuer (the leader's CTA only), commits to both CTAs;
 //   warps 2-5   scale bytes into tensor memory: the CTA's 128 weight rows and all activation rows;
 //   warps 6-13  epilogue: the accumulator into registers as bf16, which frees it for the next
-//               tile, then transposed through shared memory into 16-byte stores.
+//               tile, then transposed through shared memory into 16-byte stores;
+//   warp 14     TMA producer of the scale bytes, on rings of its own: a stage's codes take about
+//               1.3 us to come, its scales longer, through two hands, so they start earlier.
 // ---------------------------------------------------------------------------------------
 struct Pair {
-    static constexpr int THREADS = 448;
-    static constexpr int STAGES = 5, SS = 3, TS = 4;
-    static constexpr int A_BYTES = BM * KB / 2, B_BYTES = 128 * KB / 2, STAGE = A_BYTES + B_BYTES;
+    static constexpr int THREADS = 480;
+    static constexpr int TILE_A = BM * 128;                      // 128 weight rows x 256 columns of codes
+    static constexpr int CODE_BYTES = 6 * 2 * TILE_A;            // 6 stages of 256 rows, more of fewer
+    static constexpr int MAX_STAGES = 10;
+    static constexpr int SS = 4, TS = 4;                         // scale stages (512 columns) in shared / tensor memory
     static constexpr int SC_BYTES = (BM + 256) * 16;
+    // tensor memory: the accumulator, then per scale stage the bytes of 4 x 128 columns, 4
+    // columns for the weight rows and 8 for the activation rows each
     static constexpr int CH = 12, SLOT_COLS = 4 * CH, ACC_COLS = 256;
-    static constexpr int EPI_WARP = 2048;                        // 32 tokens x 32 weight rows of bf16
-    static constexpr int BARS = 2 * STAGES + 2 * SS + 2 * TS + 2;
-    static constexpr int TOTAL = STAGES * STAGE + SS * SC_BYTES + 8 * EPI_WARP + BARS * 8 + 16 + 1024;
+    static constexpr int EPI_WARP = 1024;                        // 16 activation rows x 32 weight rows of bf16
+    static constexpr int BARS = 2 * MAX_STAGES + 2 * SS + 2 * TS + 2;
+    static constexpr int TOTAL = CODE_BYTES + SS * SC_BYTES + 8 * EPI_WARP + BARS * 8 + 16 + 1024;
     static_assert(ACC_COLS + TS * SLOT_COLS <= 512, "tensor memory");
     static_assert(TOTAL <= 227 * 1024, "shared memory");
 };
@@ -444,12 +450,24 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                  ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
-__device__ __forceinline__ void umma_mxf4_pair(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t sfa,
-                                               uint32_t sfb, uint32_t accumulate) {
+// da, db: the low words of descriptors whose high word is `hi`.
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t tmem_d, uint32_t da, uint32_t db, uint32_t hi, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p; }"
-        ::"r"(tmem_d), "l"(da), "l"(db), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+        "{ .reg .pred p; .reg .b64 a, b; mov.b64 a, {%1, %3}; mov.b64 b, {%2, %3}; setp.ne.b32 p, %7, 0; "
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, [%5], [%6], p; }"
+        ::"r"(tmem_d), "r"(da), "r"(db), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+}
+// Whether the three phases are complete, by the whole warp and without waiting.
+__device__ __forceinline__ bool warp_test3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p, q, r; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; "
+        "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4; mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6; "
+        "and.pred p, p, q; and.pred p, p, r; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb), "r"(smem_u32(c)), "r"(pc) : "memory");
+    return __all_sync(0xFFFFFFFFu, done != 0);
 }
 
 template <bool EXPERTS>
@@ -459,14 +477,14 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     const int32_t* __restrict__ offsets, int experts, uint16_t* __restrict__ y, int M, int N, int K,
                     int grid_n, int grid_m, int bn) {
     using C = Pair;
-    constexpr int STAGES = C::STAGES, SS = C::SS, TS = C::TS;
+    constexpr int SS = C::SS, TS = C::TS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t* sc_smem = smem + STAGES * C::STAGE;
+    uint8_t* sc_smem = smem + C::CODE_BYTES;
     uint8_t* epi_smem = sc_smem + SS * C::SC_BYTES;
     uint64_t* full = (uint64_t*)(epi_smem + 8 * C::EPI_WARP);   // (leader's) codes of both CTAs' stage landed
-    uint64_t* empty = full + STAGES;                             // stage read by its MMAs
-    uint64_t* sfull = empty + STAGES;                            // scale bytes of 512 columns landed
+    uint64_t* empty = full + C::MAX_STAGES;                      // stage read by its MMAs
+    uint64_t* sfull = empty + C::MAX_STAGES;                     // scale bytes of 512 columns landed
     uint64_t* sempty = sfull + SS;                               // ... and read by the movers
     uint64_t* tfull = sempty + SS;                               // (leader's) both CTAs' scales in tensor memory
     uint64_t* tfree = tfull + TS;                                // ... and read by their MMAs
@@ -478,7 +496,7 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
     if (threadIdx.x == 32) {
-        for (int s = 0; s < STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+        for (int s = 0; s < C::MAX_STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
         for (int s = 0; s < SS; ++s) { mbar_init(&sfull[s], 1); mbar_init(&sempty[s], 4); }
         for (int s = 0; s < TS; ++s) { mbar_init(&tfull[s], 8); mbar_init(&tfree[s], 1); }
         mbar_init(acc_full, 1);
@@ -502,9 +520,11 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     const uint32_t tmem = *s_tmem;
     const int nk = (K + KB - 1) / KB, nsk = (nk + 1) / 2;        // stages and scale stages of a tile
     const int step = (int)gridDim.x / 2;
+    const uint32_t b_bytes = (uint32_t)bn * 64, stage_bytes = C::TILE_A + b_bytes;   // bn / 2 rows of 128 bytes
+    const int stages = min(C::MAX_STAGES, (int)(C::CODE_BYTES / stage_bytes));
 
-    auto stage_a = [&](int s) { return smem + s * C::STAGE; };
-    auto stage_b = [&](int s) { return smem + s * C::STAGE + C::A_BYTES; };
+    auto stage_a = [&](int s) { return smem + s * stage_bytes; };
+    auto stage_b = [&](int s) { return smem + s * stage_bytes + C::TILE_A; };
     auto stage_sc = [&](int s) { return sc_smem + s * C::SC_BYTES; };
     auto dead = [&](int code) {
         *(volatile int*)s_abort = 1;
@@ -522,49 +542,56 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         t = MxTile{0, mt * bn, M};
         return mt < grid_m;
     };
-    const uint32_t sc_bytes = (uint32_t)(BM + bn) * 16, b_bytes = (uint32_t)(bn / 2) * (KB / 2);
 
     if (warp == 0) {
         // ---------------- TMA producer ----------------
-        int s = 0, ss = 0, done = 0, sdone = 0;                  // stages and scale stages asked for
-        uint32_t ph = 0, sph = 0;
+        const bool one = elect_one();
+        int s = 0, done = 0;                                     // stages asked for
+        uint32_t ph = 0;
         bool ok = true;
         int n0;
         MxTile t;
-        const bool one = elect_one();
         asm volatile("griddepcontrol.wait;" ::: "memory");
         for (int lin = (int)blockIdx.x / 2; ok && get(lin, n0, t); lin += step) {
-            const int w0 = t.expert * N + n0;
+            const int w0 = t.expert * N + n0, x0 = t.t0 + rank * (bn / 2);
             for (int i = 0; i < nk; ++i) {
-                if ((i & 1) == 0) {
-                    if (!warp_wait(&sempty[ss], sph ^ 1, s_abort)) { dead(2211); ok = false; break; }
-                    if (one) {
-                        mbar_expect_tx(&sfull[ss], sc_bytes);
-                        tma_load_2d(stage_sc(ss), &map_ws, (i >> 1) * 16, w0, &sfull[ss]);
-                        tma_load_2d(stage_sc(ss) + BM * 16, &map_xs, (i >> 1) * 16, t.t0, &sfull[ss]);
-                    }
-                    __syncwarp();
-                    ++sdone;
-                    if (++ss == SS) { ss = 0; sph ^= 1; }
-                }
-                if (!warp_wait(&empty[s], ph ^ 1, s_abort)) { dead(2212); ok = false; break; }
+                if (!warp_wait(&empty[s], ph ^ 1, s_abort)) { dead(2211); ok = false; break; }
                 if (one) {
-                    if (rank == 0) mbar_expect_tx(&full[s], 2 * (C::A_BYTES + b_bytes));
+                    if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
                     const uint32_t bar = leader_addr(&full[s]);
                     tma_load_pair(stage_a(s), &map_w, i * (KB / 2), w0, bar);
-                    tma_load_pair(stage_b(s), &map_x, i * (KB / 2), t.t0 + rank * (bn / 2), bar);
+                    tma_load_pair(stage_b(s), &map_x, i * (KB / 2), x0, bar);
                 }
                 __syncwarp();
                 ++done;
-                if (++s == STAGES) { s = 0; ph ^= 1; }
+                if (++s == stages) { s = 0; ph ^= 1; }
             }
         }
-        if (!ok) {
-            // gave up: the copies in flight must land before the CTAs may end
-            if (rank == 0)
-                for (int j = max(0, done - STAGES); j < done; ++j) mbar_wait(&full[j % STAGES], (j / STAGES) & 1);
-            for (int j = max(0, sdone - SS); j < sdone; ++j) mbar_wait(&sfull[j % SS], (j / SS) & 1);
+        if (!ok && rank == 0)                                     // gave up: the copies in flight must land first
+            for (int j = max(0, done - stages); j < done; ++j) mbar_wait(&full[j % stages], (j / stages) & 1);
+    } else if (warp == 14) {
+        // ---------------- TMA producer of the scale bytes ----------------
+        const bool one = elect_one();
+        int ss = 0, done = 0, n0;
+        uint32_t ph = 0;
+        bool ok = true;
+        MxTile t;
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        for (int lin = (int)blockIdx.x / 2; ok && get(lin, n0, t); lin += step) {
+            for (int i = 0; i < nsk; ++i) {
+                if (!warp_wait(&sempty[ss], ph ^ 1, s_abort)) { dead(2212); ok = false; break; }
+                if (one) {
+                    mbar_expect_tx(&sfull[ss], (uint32_t)(BM + bn) * 16);
+                    tma_load_2d(stage_sc(ss), &map_ws, i * 16, t.expert * N + n0, &sfull[ss]);
+                    tma_load_2d(stage_sc(ss) + BM * 16, &map_xs, i * 16, t.t0, &sfull[ss]);
+                }
+                __syncwarp();
+                ++done;
+                if (++ss == SS) { ss = 0; ph ^= 1; }
+            }
         }
+        if (!ok)
+            for (int j = max(0, done - SS); j < done; ++j) mbar_wait(&sfull[j % SS], (j / SS) & 1);
     } else if (warp == 1) {
         // ---------------- MMA issuer (leader) ----------------
         if (rank == 0) {
@@ -576,33 +603,62 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             int n0;
             MxTile t;
             const bool one = elect_one();
+            const uint64_t desc = sw128_desc(smem_u32(smem));
+            const uint32_t desc_lo = (uint32_t)desc, desc_hi = (uint32_t)(desc >> 32);
             for (int lin = (int)blockIdx.x / 2; ok && get(lin, n0, t); lin += step) {
                 if (!warp_wait(acc_free, aph, s_abort)) { dead(2213); ok = false; }
-                for (int i = 0; ok && i < nk; ++i) {
-                    if ((i & 1) == 0 && !warp_wait(&tfull[ts], tph, s_abort)) { dead(2214); ok = false; break; }
-                    if (!warp_wait(&full[s], ph, s_abort)) { dead(2215); ok = false; break; }
+                // two stages a turn (the columns of one scale stage): the issuing thread's own time is
+                // what a stage must not exceed, and each wait, ready or not, takes it 140 clocks
+                for (int i = 0; ok && i < nk; i += 2) {
+                    const bool two = i + 1 < nk;
+                    const int s1 = !two ? s : s + 1 == stages ? 0 : s + 1;
+                    const uint32_t ph1 = s1 < s ? ph ^ 1 : ph;
+                    const bool ready = warp_test3(&tfull[ts], tph, &full[s], ph, &full[s1], ph1);
+                    if (!ready) {
+                        if (!warp_wait(&tfull[ts], tph, s_abort)) { dead(2214); ok = false; break; }
+                        if (!warp_wait(&full[s], ph, s_abort)) { dead(2215); ok = false; break; }
+                    }
                     asm volatile("tcgen05.fence::after_thread_sync;");
-                    const uint64_t da = sw128_desc(smem_u32(stage_a(s))), db = sw128_desc(smem_u32(stage_b(s)));
-                    const uint32_t sf = tmem + (uint32_t)(C::ACC_COLS + ts * C::SLOT_COLS + (i & 1) * 2 * C::CH);
-                    const int left = (K - i * KB) / 64;
-                    auto mma = [&](int j) {
+                    const uint32_t sf = tmem + (uint32_t)(C::ACC_COLS + ts * C::SLOT_COLS);
+                    const int left = (K - i * KB) / 64;           // K is a multiple of 64
+                    // 64 columns: j / 4 picks the stage (d: its descriptor words), j / 2 the scale words,
+                    // j % 2 their bytes
+                    auto mma = [&](int j, uint32_t d) {
                         const uint32_t id = (uint32_t)(j & 1) * 2u, sfa = sf + (uint32_t)((j >> 1) * C::CH);
-                        umma_mxf4_pair(tmem, da + 2 * j, db + 2 * j, idesc0 | id << 4 | id << 29, sfa, sfa + 4,
-                                       (i > 0 || j > 0) ? 1u : 0u);
+                        umma_mxf4_pair(tmem, d + 2 * (j & 3), d + C::TILE_A / 16 + 2 * (j & 3), desc_hi,
+                                       idesc0 | id << 4 | id << 29, sfa, sfa + 4, (i > 0 || j > 0) ? 1u : 0u);
                     };
+                    const uint32_t d0 = desc_lo + (uint32_t)s * (stage_bytes / 16);
                     if (one) {
                         if (left >= 4) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) mma(j);
+                            for (int j = 0; j < 4; ++j) mma(j, d0);
                         } else {
-                            for (int j = 0; j < left; ++j) mma(j);
+                            for (int j = 0; j < left; ++j) mma(j, d0);
                         }
                         umma_commit_pair(&empty[s]);
-                        if ((i & 1) || i + 1 == nk) umma_commit_pair(&tfree[ts]);
                     }
                     __syncwarp();
-                    if (++s == STAGES) { s = 0; ph ^= 1; }
-                    if (((i & 1) || i + 1 == nk) && ++ts == TS) { ts = 0; tph ^= 1; }
+                    if (two) {
+                        if (!ready && !warp_wait(&full[s1], ph1, s_abort)) { dead(2215); ok = false; break; }
+                        const uint32_t d1 = desc_lo + (uint32_t)s1 * (stage_bytes / 16);
+                        if (one) {
+                            if (left >= 8) {
+#pragma unroll
+                                for (int j = 4; j < 8; ++j) mma(j, d1);
+                            } else {
+                                for (int j = 4; j < left; ++j) mma(j, d1);
+                            }
+                            umma_commit_pair(&empty[s1]);
+                        }
+                        __syncwarp();
+                    }
+                    if (one) umma_commit_pair(&tfree[ts]);
+                    __syncwarp();
+                    ph = ph1;
+                    s = s1 + 1;
+                    if (s == stages) { s = 0; ph ^= 1; }
+                    if (++ts == TS) { ts = 0; tph ^= 1; }
                 }
                 // (also after giving up, and then waited for: tensor memory is not freed under a
                 // running MMA)
@@ -620,8 +676,8 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         bool ok = true;
         MxTile t;
         for (int lin = (int)blockIdx.x / 2; ok && get(lin, n0, t); lin += step) {
-            for (int it = 0; it < nsk; ++it) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sfull[ss], sph, s_abort) && mbar_wait(&tfree[ts], tph, s_abort));
+            for (int i = 0; i < nsk; ++i) {
+                ok = warp_wait(&sfull[ss], sph, s_abort) && warp_wait(&tfree[ts], tph, s_abort);
                 if (!ok) { dead(2216); break; }
                 const uint4* sc = (const uint4*)stage_sc(ss);
                 uint32_t v[C::SLOT_COLS];
@@ -660,14 +716,16 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             const int rows = min(min(bn - 128 * h, 128), t.tend - t.t0 - 128 * h);
             uint32_t p[64];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (32 * c < rows) {
-                    uint32_t v[32];
-                    tmem_ld32(src + 32u * (uint32_t)c, v);
+            for (int c = 0; c < 2; ++c) {                         // 64 columns at a time, two loads in flight
+                if (64 * c < rows) {
+                    uint32_t v[2][32];
+                    tmem_ld32(src + 64u * (uint32_t)c, v[0]);
+                    tmem_ld32(src + 64u * (uint32_t)c + 32, v[1]);
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        p[16 * c + j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                    for (int j = 0; j < 32; ++j)
+                        p[32 * c + j] = pack_bf16x2(__uint_as_float(v[j / 16][2 * (j % 16)]),
+                                                    __uint_as_float(v[j / 16][2 * (j % 16) + 1]));
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -680,21 +738,24 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                 if (32 * c >= rows) break;
                 if (wide) {
                     // two lanes swap halves, so that each holds two neighbouring weight rows of one
-                    // activation row; then 32 activation rows of 64 bytes
+                    // activation row; then 16 activation rows of 64 bytes
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const uint32_t own = p[16 * c + j], other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
-                        const uint32_t two = (lane & 1) ? prmt(other, own, 0x7632u) : prmt(own, other, 0x5410u);
-                        *(uint32_t*)(buf + (2 * j + (lane & 1)) * 64 + (lane >> 1) * 4) = two;
-                    }
-                    __syncwarp();
+                    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 32 * c + 8 * r + (lane >> 2), n = nq + 8 * (lane & 3);
-                        const uint4 o = *(const uint4*)(buf + (8 * r + (lane >> 2)) * 64 + (lane & 3) * 16);
-                        if (row < rows && n < N) *(uint4*)(yt + (size_t)row * N + n) = o;
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t own = p[16 * c + 8 * half + j], other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+                            const uint32_t two = (lane & 1) ? prmt(other, own, 0x7632u) : prmt(own, other, 0x5410u);
+                            *(uint32_t*)(buf + (2 * j + (lane & 1)) * 64 + (lane >> 1) * 4) = two;
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int row = 32 * c + 16 * half + 8 * r + (lane >> 2), n = nq + 8 * (lane & 3);
+                            const uint4 o = *(const uint4*)(buf + (8 * r + (lane >> 2)) * 64 + (lane & 3) * 16);
+                            if (row < rows && n < N) *(uint4*)(yt + (size_t)row * N + n) = o;
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 } else if (nq + lane < N) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
@@ -817,7 +878,7 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
         if (gm * gn > 0x3FFFFFFF) return fail(WQ_EUNSUPPORTED, "more than 2^30 - 1 tiles");
         if ((st = encode_u8(&mp.w, wp, k / 2, n * experts, KB / 2, BM, true, "the weight codes"))) return st;
         if ((st = encode_u8(&mp.ws, wsc, pitch, n * experts, 16, BM, false, "the weight scales"))) return st;
-        if ((st = encode_u8(&mp.x, xp, k / 2, m, KB / 2, bn / 2, true, "the activation codes"))) return st;
+        if ((st = encode_u8(&mp.x, xp, k / 2, m, 128, bn / 2, true, "the activation codes"))) return st;
         if ((st = encode_u8(&mp.xs, xsc, pitch, m, 16, bn, false, "the activation scales"))) return st;
         return offsets ? launch_pair<true>(mp, offsets, experts, y, M, N, K, gn, (int)gm, bn, overlap, s)
                        : launch_pair<false>(mp, offsets, experts, y, M, N, K, gn, (int)gm, bn, overlap, s);
