@@ -330,8 +330,9 @@ wq_status wq_gemm_w4a16(const wq_weight* w, const uint16_t* x, int64_t m, uint16
                         void* ws, size_t ws_bytes, wq_stream stream);
 
 /* Bytes of device workspace the _bf16 forms below need for the codes and scale bytes of m rows
- * of k activations. */
-size_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t k);
+ * of k activations, in a product grouped by `experts` (0: the dense product). 0 for up to 32
+ * rows, or 32 rows an expert on average, where the product quantises them itself. */
+size_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t k, int32_t experts);
 
 /* The product of two MXFP4 matrices on the block-scaled tensor cores (tcgen05 kind::mxf4):
  * y[i, r] = sum_c Wdeq[r, c] * Xdeq[i, c] for i < m, both operands as wq_dequant gives them
@@ -345,10 +346,11 @@ size_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t k);
  * no workspace, run-to-run identical. */
 wq_status wq_gemm_mxfp4(const wq_weight* w, const wq_weight* x, uint16_t* y, wq_stream stream);
 
-/* The same for bf16 activations x [m, k], which are quantised first, into the workspace, as
- * wq_quantize_mxfp4 does (m < 2^30). The two kernels overlap: the product loads weights while
- * the activations are quantised.
- *   ws  device workspace of at least wq_gemm_mxfp4_workspace_bytes(m, k) bytes. */
+/* The same for bf16 activations x [m, k], which are quantised as wq_quantize_mxfp4 does: by the
+ * product's own kernel for few rows, else first, into the workspace (m < 2^30). The two kernels
+ * then overlap: the product starts while the activations are quantised.
+ *   ws  device workspace of at least wq_gemm_mxfp4_workspace_bytes(m, k, 0) bytes (NULL if 0;
+ *       the grouped form below: with its number of experts). */
 wq_status wq_gemm_mxfp4_bf16(const wq_weight* w, const uint16_t* x, int64_t m, uint16_t* y,
                              void* ws, size_t ws_bytes, wq_stream stream);
 

@@ -57,7 +57,7 @@ _SIG = {
     "wq_quantize_lloyd": ([_vp, _i64, _i64, ctypes.POINTER(WqLloydParams), _vp, _vp, _vp, _vp,
                            _vp, _vp], _i32),
     "wq_quantize_mxfp4": ([_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp], _i32),
-    "wq_gemm_mxfp4_workspace_bytes": ([_i64, _i64], _sz),
+    "wq_gemm_mxfp4_workspace_bytes": ([_i64, _i64, _i32], _sz),
     "wq_gemm_mxfp4": ([_WP, _WP, _vp, _vp], _i32),
     "wq_gemm_mxfp4_bf16": ([_WP, _vp, _i64, _vp, _vp, _sz, _vp], _i32),
     "wq_gemm_mxfp4_experts": ([_WP, _i32, _vp, _WP, _vp, _vp], _i32),
@@ -430,8 +430,9 @@ def gemm_static(w: PackedWeight, x: torch.Tensor, out: torch.Tensor | None = Non
 
 
 @functools.lru_cache(maxsize=4096)
-def _mx_workspace_bytes(m: int, k: int) -> int:
-    return int(_lib.wq_gemm_mxfp4_workspace_bytes(m, k))
+def gemm_mxfp4_workspace_bytes(m: int, k: int, experts: int = 0) -> int:
+    """Bytes of workspace gemm_mxfp4 (experts=0) and gemm_experts_mxfp4 need for bf16 activations."""
+    return int(_lib.wq_gemm_mxfp4_workspace_bytes(m, k, experts))
 
 
 def _mx_product(w: PackedWeight, x, out, workspace, offsets):
@@ -473,8 +474,8 @@ def _mx_product(w: PackedWeight, x, out, workspace, offsets):
         else:
             _check(_lib.wq_gemm_mxfp4(ctypes.byref(d), ctypes.byref(xd), _ptr(out), _stream(t)))
         return out
-    need = _mx_workspace_bytes(m, k)
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
+    need = gemm_mxfp4_workspace_bytes(m, k, experts)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = x.new_empty((need + 1) // 2)
     if experts:
         _check(_lib.wq_gemm_mxfp4_experts_bf16(ctypes.byref(d), experts, _ptr(offsets), _ptr(x), m, _ptr(out),
@@ -488,7 +489,7 @@ def gemm_mxfp4(w: PackedWeight, x, out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y = x W^T with both operands MXFP4, on the block-scaled tensor cores -> bf16 [m, n]. x is
     quantize_mxfp4's result for [m, k] activations, or a bf16 [m, k] tensor, which is quantised
-    first (into `workspace` if given, see wq_gemm_mxfp4_workspace_bytes). k % 64 == 0."""
+    on the way (more than 32 rows: into `workspace`, allocated if not given). k % 64 == 0."""
     return _mx_product(w, x, out, workspace, None)
 
 

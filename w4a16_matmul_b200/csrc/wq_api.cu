@@ -590,8 +590,8 @@ wq_status mx_product(const wq_weight* w, int32_t experts, const int32_t* offsets
         return fail(WQ_EINVAL, "x has k=%lld columns, w has %lld", (long long)x->k, (long long)w->k);
     if ((st = check_injected())) return st;
     const int e = experts ? experts : 1;
-    return launch_gemm_mxfp4(w->packed, (const uint8_t*)w->aux, x->packed, (const uint8_t*)x->aux, x->n, w->n / e, w->k,
-                             e, offsets, y, false, s);
+    return launch_gemm_mxfp4(w->packed, (const uint8_t*)w->aux, x->packed, (const uint8_t*)x->aux, nullptr, x->n,
+                             w->n / e, w->k, e, offsets, y, false, s);
 }
 
 wq_status mx_product_bf16(const wq_weight* w, int32_t experts, const int32_t* offsets, const uint16_t* x, int64_t m,
@@ -600,24 +600,30 @@ wq_status mx_product_bf16(const wq_weight* w, int32_t experts, const int32_t* of
     wq_status st = check_mx_product(w, experts, offsets, m, y);
     if (st) return st;
     if ((st = check_ptr(x, "x", false))) return st;
-    if ((st = check_ptr(ws, "ws", false))) return st;
-    const size_t need = wq_gemm_mxfp4_workspace_bytes(m, w->k);
-    if (ws_bytes < need)
-        return fail(WQ_EINVAL, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes, need);
+    const size_t need = wq_gemm_mxfp4_workspace_bytes(m, w->k, experts);
+    if (need > 0) {
+        if ((st = check_ptr(ws, "ws", false))) return st;
+        if (ws_bytes < need)
+            return fail(WQ_EINVAL, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes, need);
+    }
     if ((st = check_injected())) return st;
+    const int e = experts ? experts : 1;
+    const uint8_t* wsc = (const uint8_t*)w->aux;
+    if (need == 0)
+        return launch_gemm_mxfp4(w->packed, wsc, nullptr, nullptr, x, m, w->n / e, w->k, e, offsets, y, false, s);
     uint8_t* codes = (uint8_t*)ws;
     uint8_t* scale = codes + mx_x_code_bytes(m, w->k);
     if ((st = launch_quantize_mxfp4(x, WQ_BF16, m, w->k, scale, nullptr, codes, nullptr, s))) return st;
-    const int e = experts ? experts : 1;
-    return launch_gemm_mxfp4(w->packed, (const uint8_t*)w->aux, codes, scale, m, w->n / e, w->k, e, offsets, y, true, s);
+    return launch_gemm_mxfp4(w->packed, wsc, codes, scale, nullptr, m, w->n / e, w->k, e, offsets, y, true, s);
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t k) {
-    if (m < 1 || k < 1 || m >= (1LL << 30) || k > (1LL << 31) - 1) return 0;
+size_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t k, int32_t experts) {
+    if (m < 1 || k < 1 || m >= (1LL << 30) || k > (1LL << 31) - 1 || experts < 0) return 0;
+    if (mx_quantises_itself(m, experts ? experts : 1)) return 0;
     return mx_x_code_bytes(m, k) + (size_t)m * (size_t)mx_pitch(k);
 }
 

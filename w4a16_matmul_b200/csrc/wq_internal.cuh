@@ -180,11 +180,14 @@ wq_status launch_quantize_mxfp4(const void* x, int dtype, int64_t n, int64_t k, 
                                 uint8_t* packed, void* q, cudaStream_t s);
 wq_status launch_dequant_mxfp4(const wq_weight& w, uint16_t* out, cudaStream_t s);
 // y = x W^T for MXFP4 x [m, k] and W [experts * n, k]: rows [offsets[e], offsets[e + 1]) of x
-// with the n rows of expert e; offsets NULL (experts 1): all rows. `overlap`: the kernel may
-// start beside the one before it in the stream, which writes x's codes and nothing else it reads.
-wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t* xp, const uint8_t* xsc, int64_t m,
-                            int64_t n, int64_t k, int experts, const int32_t* offsets, uint16_t* y, bool overlap,
-                            cudaStream_t s);
+// with the n rows of expert e; offsets NULL (experts 1): all rows. x is given as codes and scale
+// bytes, or (x16, where mx_quantises_itself) as bf16, which the kernel then quantises. `overlap`:
+// the kernel may start beside the one before it in the stream, which writes x's codes and nothing
+// else it reads.
+bool mx_quantises_itself(int64_t m, int experts);
+wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t* xp, const uint8_t* xsc,
+                            const uint16_t* x16, int64_t m, int64_t n, int64_t k, int experts, const int32_t* offsets,
+                            uint16_t* y, bool overlap, cudaStream_t s);
 wq_status read_mx_error(int32_t* code);
 
 // Number of SMs of the current device (cached per device).
@@ -371,6 +374,34 @@ __device__ __forceinline__ void mx4_word(uint32_t w, uint32_t (&p)[4]) {
 __device__ __forceinline__ uint32_t mx_scale_pair(uint32_t s) {
     const uint32_t b = s << 7 | ((s == 0 || s == 255) ? 0x40u : 0u);
     return b * 0x10001u;
+}
+
+// MXFP4 quantisation: the scale byte of a block whose largest magnitude has the exponent field
+// `field` (255 marks a NaN or an infinity), and 2^(127 - s) (any finite number for 255).
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t field) {
+    return field == 255 ? 255u : field > 2 ? field - 2 : 0u;
+}
+__device__ __forceinline__ float mx_inverse_scale(uint32_t s) {
+    return __uint_as_float((254u - (s < 252u ? s : 252u)) << 23);
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// E2M1 codes of 8 values, value j in nibble j.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{ .reg .b8 a, b, c, d; "
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; "
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3; "
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; "
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7; "
+        "mov.b32 %0, {a, b, c, d}; }"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
 }
 
 // bf16x2 -> fp16x2 (round to nearest even; exact for |x| in [2^-14, 65504]).

@@ -26,26 +26,6 @@ int stream_grid(int64_t items, int per_sm_blocks = 8) {
     return (int)(blocks < 1 ? 1 : blocks);
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// E2M1 codes of 8 values, value j in nibble j.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
-    uint32_t r;
-    asm("{ .reg .b8 a, b, c, d; "
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; "
-        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3; "
-        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; "
-        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7; "
-        "mov.b32 %0, {a, b, c, d}; }"
-        : "=r"(r)
-        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
-    return r;
-}
-
 __device__ __forceinline__ void ldg_v8(const float* p, uint32_t (&v)[8]) {
     asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
@@ -106,10 +86,9 @@ __device__ __forceinline__ void quantise_chunk(const Chunk<F32>& ch, bool live, 
     }
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    const uint32_t field = top >> 23;
-    const bool bad = field == 255;                             // a NaN or an infinity in the block
-    const uint32_t s = bad ? 255u : field > 2 ? field - 2 : 0u;
-    const float inv = __uint_as_float((254u - min(s, 252u)) << 23);   // 2^(127 - s)
+    const uint32_t s = mx_scale_byte(top >> 23);
+    const bool bad = s == 255;                                 // a NaN or an infinity in the block
+    const float inv = mx_inverse_scale(s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= inv;
     const uint32_t p = bad ? 0u : e2m1x8(v);

@@ -11,7 +11,7 @@
 //              bytes] and of the activation tile [BN x 128 bytes], 128-byte swizzle; per 512
 //              columns the scale bytes of both [128 + BN rows x 16 bytes];
 //   warp 1     allocates tensor memory, and one lane issues the MMAs (K = 64 each);
-//   warps 2-5  move the scale bytes into tensor memory: the MMA wants the four bytes of row r's
+//   warps 2-5  (few rows: quantise the activations; see XQ below) move the scale bytes into tensor memory: the MMA wants the four bytes of row r's
 //              128 columns in lane r % 32 of column r / 32, in each of the four lane quarters,
 //              so each warp fills its own quarter; afterwards they drain the accumulator.
 // Grouped by expert, a CTA finds its expert and its rows from the offsets on the device: the
@@ -138,13 +138,71 @@ __device__ __forceinline__ MxTile find_tile(const int32_t* __restrict__ offsets,
     return MxTile{-1, 0, 0};
 }
 
-template <int BN, int CL, bool EXPERTS>
+// Activations as they come, for tiles of at most 32 rows (XQ): warps 2-5 quantise them on the way
+// into the stage, a block of 32 columns a thread at a time, one scale stage ahead in registers.
+// Every CTA of a row tile repeats that work, which few rows make cheap; it saves the kernel in
+// front, its workspace, and the wait for it.
+template <int BN>
+struct XBlocks {
+    static constexpr int PER = BN * 16 / 128;    // blocks of 32 a thread has in a scale stage of 512 columns
+    uint4 v[PER][4];
+};
+// Block j of thread m (0..127): activation row 8 j + m / 16, columns 32 (m % 16) .. + 31. Rows
+// from `rows` on are left out: what their accumulator columns hold is not stored.
+template <int BN>
+__device__ __forceinline__ void load_x_blocks(XBlocks<BN>& xb, const uint16_t* __restrict__ x, int m, int t0, int rows,
+                                              int col0, int K) {
+    const int col = col0 + 32 * (m % 16);
+#pragma unroll
+    for (int j = 0; j < XBlocks<BN>::PER; ++j) {
+        const int row = 8 * j + m / 16;
+        const uint16_t* p = x + (size_t)(t0 + row) * K + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xb.v[j][i] = row < rows && col < K ? ldg_v4(p + 8 * i) : make_uint4(0, 0, 0, 0);
+    }
+}
+// 32 bf16 values -> their codes and scale byte, as the quantisation kernel makes them.
+__device__ __forceinline__ uint32_t quantise32(const uint4 (&v)[4], uint4& codes) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        top = max_u16x2(top, max_u16x2(max_u16x2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                       max_u16x2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
+    const uint32_t s = mx_scale_byte(max(top & 0xFFFFu, top >> 16) >> 7);
+    const float inv = mx_inverse_scale(s);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = __uint_as_float(w[j] << 16) * inv;
+            f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
+        }
+        c[i] = s == 255 ? 0u : e2m1x8(f);
+    }
+    codes = make_uint4(c[0], c[1], c[2], c[3]);
+    return s;
+}
+// A barrier of warps 2-5 that also tells whether all of them are well.
+__device__ __forceinline__ bool movers_all(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.and.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
+        : "=r"(r) : "r"((uint32_t)ok) : "memory");
+    return r != 0;
+}
+
+template <int BN, int CL, bool EXPERTS, bool XQ>
 __global__ void __launch_bounds__(kThreads, 2)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_ws,
                const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_xs,
-               const int32_t* __restrict__ offsets, int experts, uint16_t* __restrict__ y, int M, int N, int K,
-               int grid_n, int kt_per_split) {
+               const uint16_t* __restrict__ x16, const int32_t* __restrict__ offsets, int experts,
+               uint16_t* __restrict__ y, int M, int N, int K, int grid_n, int kt_per_split) {
+    static_assert(!XQ || BN <= 32, "few rows");
     using C = Cfg<BN>;
+    constexpr uint32_t kScTx = XQ ? BM * 16 : C::SC_BYTES, kCodeTx = XQ ? C::A_BYTES : C::STAGE;
     constexpr int STAGES = C::STAGES, SS = C::SSTAGES, TS = C::TSLOTS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -174,7 +232,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (threadIdx.x == 0) {
-        prefetch_map(&map_w); prefetch_map(&map_ws); prefetch_map(&map_x); prefetch_map(&map_xs);
+        prefetch_map(&map_w); prefetch_map(&map_ws);
+        if (!XQ) { prefetch_map(&map_x); prefetch_map(&map_xs); }
     }
     MxTile tile{0, (lin / grid_n) * BN, M};
     if (EXPERTS) {
@@ -182,13 +241,6 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             MxScan at;
             tile = find_tile(offsets, experts, M, lin / grid_n, BN, at);
             if (lane == 0) { s_tile[0] = tile.expert; s_tile[1] = tile.t0; s_tile[2] = tile.tend; }
-        }
-        __syncthreads();
-        tile = MxTile{s_tile[0], s_tile[1], s_tile[2]};
-        if (tile.expert < 0) {                                   // (clusters are not used here)
-            // not to be complete before the kernel this launch overlaps
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            return;
         }
     }
     if (warp == 1) {
@@ -200,11 +252,23 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;");
     const uint32_t tmem = *s_tmem;
+    if (EXPERTS) {
+        tile = MxTile{s_tile[0], s_tile[1], s_tile[2]};
+        if (tile.expert < 0) {                                   // (clusters are not used here)
+            if (warp == 1)
+                asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
+            // not to be complete before the kernel this launch overlaps
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            return;
+        }
+    }
     const int KT = (K + KB - 1) / KB;
     const int kt0 = crank * kt_per_split;                        // even: scale stages do not straddle splits
     const int nk = max(0, min(KT, kt0 + kt_per_split) - kt0);
     const int t0 = tile.t0, tend = tile.tend;
     const int w0 = tile.expert * N + n0;                         // first weight row of the tile in the stack
+    XBlocks<XQ ? BN : 16> xb;
+    if (XQ && warp >= 2) load_x_blocks(xb, x16, (int)threadIdx.x - 64, t0, tend - t0, kt0 * KB, K);
 
     auto stage_a = [&](int s) { return smem + s * C::STAGE; };
     auto stage_b = [&](int s) { return smem + s * C::STAGE + C::A_BYTES; };
@@ -222,14 +286,14 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         if (one) {
             for (int i = 0; i < pre; ++i) {
                 if ((i & 1) == 0) {
-                    mbar_expect_tx(&sfull[i >> 1], C::SC_BYTES);
+                    mbar_expect_tx(&sfull[i >> 1], kScTx);
                     tma_load_2d(stage_sc(i >> 1), &map_ws, ((kt0 + i) >> 1) * 16, w0, &sfull[i >> 1]);
                 }
-                mbar_expect_tx(&full[i], C::STAGE);
+                mbar_expect_tx(&full[i], kCodeTx);
                 tma_load_2d(stage_a(i), &map_w, (kt0 + i) * (KB / 2), w0, &full[i]);
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            for (int i = 0; i < pre; ++i) {
+            for (int i = 0; !XQ && i < pre; ++i) {
                 if ((i & 1) == 0)
                     tma_load_2d(stage_sc(i >> 1) + BM * 16, &map_xs, ((kt0 + i) >> 1) * 16, t0, &sfull[i >> 1]);
                 tma_load_2d(stage_b(i), &map_x, (kt0 + i) * (KB / 2), t0, &full[i]);
@@ -243,9 +307,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             if ((i & 1) == 0) {
                 if (!warp_wait(&sempty[ss], sph ^ 1, s_abort)) { dead(2201); break; }
                 if (one) {
-                    mbar_expect_tx(&sfull[ss], C::SC_BYTES);
+                    mbar_expect_tx(&sfull[ss], kScTx);
                     tma_load_2d(stage_sc(ss), &map_ws, ((kt0 + i) >> 1) * 16, w0, &sfull[ss]);
-                    tma_load_2d(stage_sc(ss) + BM * 16, &map_xs, ((kt0 + i) >> 1) * 16, t0, &sfull[ss]);
+                    if (!XQ) tma_load_2d(stage_sc(ss) + BM * 16, &map_xs, ((kt0 + i) >> 1) * 16, t0, &sfull[ss]);
                 }
                 __syncwarp();
                 ++sdone;
@@ -253,9 +317,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             }
             if (!warp_wait(&empty[s], ph ^ 1, s_abort)) { dead(2202); break; }
             if (one) {
-                mbar_expect_tx(&full[s], C::STAGE);
+                mbar_expect_tx(&full[s], kCodeTx);
                 tma_load_2d(stage_a(s), &map_w, (kt0 + i) * (KB / 2), w0, &full[s]);
-                tma_load_2d(stage_b(s), &map_x, (kt0 + i) * (KB / 2), t0, &full[s]);
+                if (!XQ) tma_load_2d(stage_b(s), &map_x, (kt0 + i) * (KB / 2), t0, &full[s]);
             }
             __syncwarp();
             if (++s == STAGES) { s = 0; ph ^= 1; }
@@ -309,14 +373,43 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         // ---------------- scale bytes into tensor memory, then the epilogue ----------------
         const int q = warp & 3;                                   // this warp's lane quarter
         const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
-        int ss = 0, t = 0;
-        uint32_t sph = 0, tph = 0;
+        int ss = 0, t = 0, cs = 0;                                // scale stage, slot, code stage (XQ)
+        uint32_t sph = 0, tph = 0, cph = 0;
         const int nt = (nk + 1) / 2;
         for (int it = 0; it < nt; ++it) {
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sfull[ss], sph, s_abort) &&
-                                         (it < TS || mbar_wait(&tfree[t], tph ^ 1, s_abort)))) {
-                dead(2205); break;
+            bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sfull[ss], sph, s_abort) &&
+                                              (it < TS || mbar_wait(&tfree[t], tph ^ 1, s_abort)));
+            if (XQ) {
+                const int m = (int)threadIdx.x - 64, b = m % 16;  // (b: block of the scale stage)
+                // the scale stage's code stages, each free again
+                const bool two = 2 * it + 1 < nk;
+                ok = ok && warp_wait(&empty[cs], cph ^ 1, s_abort);
+                int cs1 = cs + 1;
+                uint32_t cph1 = cph;
+                if (cs1 == STAGES) { cs1 = 0; cph1 ^= 1; }
+                if (two) ok = ok && warp_wait(&empty[cs1], cph1 ^ 1, s_abort);
+                if (ok && (b < 8 || two)) {
+                    uint8_t* tile_b = stage_b(b < 8 ? cs : cs1);
+#pragma unroll
+                    for (int j = 0; j < XBlocks<BN>::PER; ++j) {
+                        const int row = 8 * j + m / 16;
+                        if (t0 + row < tend) {
+                            uint4 codes;
+                            const uint32_t sb = quantise32(xb.v[j], codes);
+                            // the 128-byte swizzle of the tile's rows
+                            *(uint4*)(tile_b + row * 128 + (((b & 7) ^ (row & 7)) * 16)) = codes;
+                            stage_sc(ss)[BM * 16 + row * 16 + b] = (uint8_t)sb;
+                        }
+                    }
+                }
+                cs = cs1 + 1;
+                cph = cph1;
+                if (cs == STAGES) { cs = 0; cph ^= 1; }
+                if (it + 1 < nt) load_x_blocks(xb, x16, m, t0, tend - t0, kt0 * KB + (it + 1) * 2 * KB, K);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMAs read the codes
+                ok = movers_all(ok);
             }
+            if (!ok) { dead(2205); break; }
             const uint4* sc = (const uint4*)stage_sc(ss);
             uint32_t v[C::SLOT_COLS];
 #pragma unroll
@@ -799,10 +892,10 @@ wq_status encode_u8(CUtensorMap* map, const void* base, int64_t row_bytes, int64
     return WQ_OK;
 }
 
-template <int BN, int CL, bool EXPERTS>
-wq_status launch_one(const Maps& mp, const int32_t* offsets, int experts, uint16_t* y, int M, int N, int K,
+template <int BN, int CL, bool EXPERTS, bool XQ>
+wq_status launch_one(const Maps& mp, const uint16_t* x16, const int32_t* offsets, int experts, uint16_t* y, int M, int N, int K,
                      int grid_n, int64_t grid_m, int kt_per_split, bool overlap, cudaStream_t s) {
-    auto k = mx_gemm_kernel<BN, CL, EXPERTS>;
+    auto k = mx_gemm_kernel<BN, CL, EXPERTS, XQ>;
     constexpr int smem = Cfg<BN>::TOTAL;
     static bool raised = false;        // the shared-memory opt-in holds for the process
     if (!raised && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess)
@@ -828,7 +921,7 @@ wq_status launch_one(const Maps& mp, const int32_t* offsets, int experts, uint16
     }
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    cudaLaunchKernelEx(&cfg, k, mp.w, mp.ws, mp.x, mp.xs, offsets, experts, y, M, N, K, grid_n, kt_per_split);
+    cudaLaunchKernelEx(&cfg, k, mp.w, mp.ws, mp.x, mp.xs, x16, offsets, experts, y, M, N, K, grid_n, kt_per_split);
     return check_launch("mxfp4 gemm");
 }
 
@@ -856,9 +949,11 @@ wq_status launch_pair(const Maps& mp, const int32_t* offsets, int experts, uint1
 
 }  // namespace
 
-wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t* xp, const uint8_t* xsc, int64_t m,
-                            int64_t n, int64_t k, int experts, const int32_t* offsets, uint16_t* y, bool overlap,
-                            cudaStream_t s) {
+bool mx_quantises_itself(int64_t m, int experts) { return (m + experts - 1) / experts <= 32; }
+
+wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t* xp, const uint8_t* xsc,
+                            const uint16_t* x16, int64_t m, int64_t n, int64_t k, int experts, const int32_t* offsets,
+                            uint16_t* y, bool overlap, cudaStream_t s) {
     const int M = (int)m, N = (int)n, K = (int)k;
     const int grid_n = (N + BM - 1) / BM;
     const int KT = (K + KB - 1) / KB;
@@ -901,18 +996,22 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
     per += per & 1;
     if ((st = encode_u8(&mp.w, wp, k / 2, n * experts, KB / 2, BM, true, "the weight codes"))) return st;
     if ((st = encode_u8(&mp.ws, wsc, pitch, n * experts, 16, BM, false, "the weight scales"))) return st;
-    if ((st = encode_u8(&mp.x, xp, k / 2, m, KB / 2, bn, true, "the activation codes"))) return st;
-    if ((st = encode_u8(&mp.xs, xsc, pitch, m, 16, bn, false, "the activation scales"))) return st;
-#define WQ_MX(BN, CL, EX) \
-    launch_one<BN, CL, EX>(mp, offsets, experts, y, M, N, K, grid_n, grid_m, per, overlap, s)
-#define WQ_MX_CL(BN) \
-    (offsets ? WQ_MX(BN, 1, true) : cl == 8 ? WQ_MX(BN, 8, false) : cl == 4 ? WQ_MX(BN, 4, false) \
-             : cl == 2 ? WQ_MX(BN, 2, false) : WQ_MX(BN, 1, false))
+    if (!x16) {
+        if ((st = encode_u8(&mp.x, xp, k / 2, m, KB / 2, bn, true, "the activation codes"))) return st;
+        if ((st = encode_u8(&mp.xs, xsc, pitch, m, 16, bn, false, "the activation scales"))) return st;
+    } else {
+        mp.x = mp.xs = mp.w;                                     // not used
+    }
+#define WQ_MX(BN, CL, EX, XQ) \
+    launch_one<BN, CL, EX, XQ>(mp, x16, offsets, experts, y, M, N, K, grid_n, grid_m, per, overlap, s)
+#define WQ_MX_CL(BN, XQ)                                                                           \
+    (offsets ? WQ_MX(BN, 1, true, XQ) : cl == 8 ? WQ_MX(BN, 8, false, XQ) : cl == 4 ? WQ_MX(BN, 4, false, XQ) \
+             : cl == 2 ? WQ_MX(BN, 2, false, XQ) : WQ_MX(BN, 1, false, XQ))
     switch (bn) {
-        case 16: return WQ_MX_CL(16);
-        case 32: return WQ_MX_CL(32);
-        case 64: return WQ_MX_CL(64);
-        default: return WQ_MX_CL(128);
+        case 16: return x16 ? WQ_MX_CL(16, true) : WQ_MX_CL(16, false);
+        case 32: return x16 ? WQ_MX_CL(32, true) : WQ_MX_CL(32, false);
+        case 64: return WQ_MX_CL(64, false);
+        default: return WQ_MX_CL(128, false);
     }
 #undef WQ_MX_CL
 #undef WQ_MX
