@@ -185,12 +185,12 @@ __device__ __forceinline__ uint32_t quantise32(const uint4 (&v)[4], uint4& codes
     codes = make_uint4(c[0], c[1], c[2], c[3]);
     return s;
 }
-// A barrier of warps 2-5 that also tells whether all of them are well.
-__device__ __forceinline__ bool movers_all(bool ok) {
+// Barrier `id` of `threads` threads (whole warps) that also tells whether all of them are well.
+__device__ __forceinline__ bool bar_all(int id, int threads, bool ok) {
     uint32_t r;
     asm volatile(
-        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.and.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
-        : "=r"(r) : "r"((uint32_t)ok) : "memory");
+        "{ .reg .pred p, q; setp.ne.u32 p, %3, 0; barrier.cta.red.and.pred q, %1, %2, p; selp.u32 %0, 1, 0, q; }"
+        : "=r"(r) : "r"(id), "r"(threads), "r"((uint32_t)ok) : "memory");
     return r != 0;
 }
 
@@ -407,7 +407,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                 if (cs == STAGES) { cs = 0; cph ^= 1; }
                 if (it + 1 < nt) load_x_blocks(xb, x16, m, t0, tend - t0, kt0 * KB + (it + 1) * 2 * KB, K);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMAs read the codes
-                ok = movers_all(ok);
+                ok = bar_all(1, 128, ok);                         // warps 2-5
             }
             if (!ok) { dead(2205); break; }
             const uint4* sc = (const uint4*)stage_sc(ss);
@@ -502,23 +502,23 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 //   warp 1      MMA issuer (the leader's CTA only), commits to both CTAs;
 //   warps 2-5   scale bytes into tensor memory: the CTA's 128 weight rows and all activation rows;
 //   warps 6-13  epilogue: the accumulator into registers as bf16, which frees it for the next
-//               tile, then transposed through shared memory into 16-byte stores;
+//               tile, then transposed (stmatrix) into rows of 64 weight rows, which TMA stores;
 //   warp 14     TMA producer of the scale bytes, on rings of its own: a stage's codes take about
 //               1.3 us to come, its scales longer, through two hands, so they start earlier.
 // ---------------------------------------------------------------------------------------
 struct Pair {
     static constexpr int THREADS = 480;
     static constexpr int TILE_A = BM * 128;                      // 128 weight rows x 256 columns of codes
-    static constexpr int CODE_BYTES = 6 * 2 * TILE_A;            // 6 stages of 256 rows, more of fewer
+    static constexpr int CODE_BYTES = 5 * 2 * TILE_A;            // 5 stages of 256 rows, more of fewer
     static constexpr int MAX_STAGES = 10;
     static constexpr int SS = 4, TS = 4;                         // scale stages (512 columns) in shared / tensor memory
     static constexpr int SC_BYTES = (BM + 256) * 16;
     // tensor memory: the accumulator, then per scale stage the bytes of 4 x 128 columns, 4
     // columns for the weight rows and 8 for the activation rows each
     static constexpr int CH = 12, SLOT_COLS = 4 * CH, ACC_COLS = 256;
-    static constexpr int EPI_WARP = 1024;                        // 16 activation rows x 32 weight rows of bf16
+    static constexpr int EPI_TILE = 32 * 128;                    // 32 activation rows x 64 weight rows of bf16
     static constexpr int BARS = 2 * MAX_STAGES + 2 * SS + 2 * TS + 2;
-    static constexpr int TOTAL = CODE_BYTES + SS * SC_BYTES + 8 * EPI_WARP + BARS * 8 + 16 + 1024;
+    static constexpr int TOTAL = CODE_BYTES + 8 * EPI_TILE + SS * SC_BYTES + BARS * 8 + 16 + 1024;
     static_assert(ACC_COLS + TS * SLOT_COLS <= 512, "tensor memory");
     static_assert(TOTAL <= 227 * 1024, "shared memory");
 };
@@ -567,15 +567,16 @@ template <bool EXPERTS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
 mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_ws,
                     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_xs,
+                    const __grid_constant__ CUtensorMap map_y,
                     const int32_t* __restrict__ offsets, int experts, uint16_t* __restrict__ y, int M, int N, int K,
                     int grid_n, int grid_m, int bn) {
     using C = Pair;
     constexpr int SS = C::SS, TS = C::TS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t* sc_smem = smem + C::CODE_BYTES;
-    uint8_t* epi_smem = sc_smem + SS * C::SC_BYTES;
-    uint64_t* full = (uint64_t*)(epi_smem + 8 * C::EPI_WARP);   // (leader's) codes of both CTAs' stage landed
+    uint8_t* epi_smem = smem + C::CODE_BYTES;
+    uint8_t* sc_smem = epi_smem + 8 * C::EPI_TILE;
+    uint64_t* full = (uint64_t*)(sc_smem + SS * C::SC_BYTES);   // (leader's) codes of both CTAs' stage landed
     uint64_t* empty = full + C::MAX_STAGES;                      // stage read by its MMAs
     uint64_t* sfull = empty + C::MAX_STAGES;                     // scale bytes of 512 columns landed
     uint64_t* sempty = sfull + SS;                               // ... and read by the movers
@@ -599,7 +600,7 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (threadIdx.x == 0) {
-        prefetch_map(&map_w); prefetch_map(&map_ws); prefetch_map(&map_x); prefetch_map(&map_xs);
+        prefetch_map(&map_w); prefetch_map(&map_ws); prefetch_map(&map_x); prefetch_map(&map_xs); prefetch_map(&map_y);
     }
     __syncwarp();
     if (warp == 1) {
@@ -794,70 +795,94 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         // ---------------- epilogue ----------------
         const int q = warp & 3, h = (warp - 6) >> 2;              // lane quarter; columns 128 h .. 128 h + 127
         const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(128 * h);
-        uint8_t* buf = epi_smem + (warp - 6) * C::EPI_WARP;
+        // two warps of neighbouring quarters fill a store tile together (barrier `id`), in two
+        // buffers in turn; its first warp's lane 0 issues the stores
+        const int team = 2 * h + (q >> 1), id = 1 + team;
+        const bool issuer = (q & 1) == 0 && lane == 0;
+        uint8_t* bufs = epi_smem + 2 * team * C::EPI_TILE;
         const bool wide = (N & 7) == 0;                           // rows of y are then 16-byte aligned
-        uint32_t aph = 0;
+        uint32_t aph = 0, flip = 0;
         bool ok = true;
         int n0;
         MxTile t;
         for (int lin = (int)blockIdx.x / 2; ok && get(lin, n0, t); lin += step, aph ^= 1) {
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, aph, s_abort)) &&
                  !__any_sync(0xFFFFFFFFu, *(volatile int*)s_abort != 0);
-            if (!ok) { dead(2217); break; }
+            if (!bar_all(id, 64, ok)) { ok = false; dead(2217); break; }
             asm volatile("tcgen05.fence::after_thread_sync;");
             // activation rows of this tile that this warp holds
             const int rows = min(min(bn - 128 * h, 128), t.tend - t.t0 - 128 * h);
+            // p[16 c + 4 g + 2 l + r]: weight rows 16 l + 8 r .. + 7 of the quarter, activation rows 32 c +
+            // 8 g .. + 7, as the 8 x 8 fragments that stmatrix takes
             uint32_t p[64];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {                         // 64 columns at a time, two loads in flight
-                if (64 * c < rows) {
-                    uint32_t v[2][32];
-                    tmem_ld32(src + 64u * (uint32_t)c, v[0]);
-                    tmem_ld32(src + 64u * (uint32_t)c + 32, v[1]);
+            for (int c = 0; c < 4; ++c) {
+                if (32 * c < rows) {
+                    uint32_t v[2][16];
+                    tmem_ld_16x256b_x4(src + 32u * (uint32_t)c, v[0]);
+                    tmem_ld_16x256b_x4(src + 32u * (uint32_t)c + (16u << 16), v[1]);
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        p[32 * c + j] = pack_bf16x2(__uint_as_float(v[j / 16][2 * (j % 16)]),
-                                                    __uint_as_float(v[j / 16][2 * (j % 16) + 1]));
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int l = 0; l < 2; ++l)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                p[16 * c + 4 * g + 2 * l + r] =
+                                    pack_bf16x2(__uint_as_float(v[l][4 * g + 2 * r]), __uint_as_float(v[l][4 * g + 2 * r + 1]));
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive_leader(acc_free);
-            const int nq = n0 + 32 * q;                           // this warp's first weight row
-            uint16_t* yt = y + (size_t)(t.t0 + 128 * h) * N;
+            const int nt = n0 + 64 * (q >> 1);                    // the store tile's first weight row
+            const int r0 = t.t0 + 128 * h;                        // ... and activation row
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 if (32 * c >= rows) break;
-                if (wide) {
-                    // two lanes swap halves, so that each holds two neighbouring weight rows of one
-                    // activation row; then 16 activation rows of 64 bytes
+                uint8_t* buf = bufs + flip * C::EPI_TILE;
+                flip ^= 1;
+                // 128-byte rows in the swizzle that the store undoes, free of bank conflicts
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                for (int g = 0; g < 2; ++g)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t own = p[16 * c + 8 * half + j], other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
-                            const uint32_t two = (lane & 1) ? prmt(other, own, 0x7632u) : prmt(own, other, 0x5410u);
-                            *(uint32_t*)(buf + (2 * j + (lane & 1)) * 64 + (lane >> 1) * 4) = two;
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const int row = 32 * c + 16 * half + 8 * r + (lane >> 2), n = nq + 8 * (lane & 3);
-                            const uint4 o = *(const uint4*)(buf + (8 * r + (lane >> 2)) * 64 + (lane & 3) * 16);
-                            if (row < rows && n < N) *(uint4*)(yt + (size_t)row * N + n) = o;
-                        }
-                        __syncwarp();
+                    for (int l = 0; l < 2; ++l) {
+                        const int row = 16 * g + 8 * (lane >> 4) + (lane & 7), col = 4 * (q & 1) + 2 * l + ((lane >> 3) & 1);
+                        const uint32_t* f = p + 16 * c + 8 * g + 2 * l;
+                        stmatrix_x4_trans(smem_u32(buf) + (uint32_t)(row * 128 + ((col ^ (row & 7)) * 16)), f[0], f[1], f[4], f[5]);
                     }
-                } else if (nq + lane < N) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const uint32_t two = p[16 * c + j / 2];
-                        if (32 * c + j < rows) yt[(size_t)(32 * c + j) * N + nq + lane] = (uint16_t)(j & 1 ? two >> 16 : two);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                // the other buffer's store has been read out by the time anyone passes
+                if (issuer) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                bar_all(id, 64, true);
+                if (wide && 32 * c + 32 <= rows) {
+                    if (issuer && nt < N) {
+                        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                                     ::"l"(&map_y), "r"(nt), "r"(r0 + 32 * c), "r"(smem_u32(buf)) : "memory");
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
+                    __syncwarp();
+                } else {
+                    // the last rows of an expert (or of all), or rows of y that are not aligned
+                    const int m = 32 * (q & 1) + lane;
+                    const int left = min(32, rows - 32 * c);
+                    uint16_t* yt = y + (size_t)(r0 + 32 * c) * N + nt;
+                    if (wide) {
+                        for (int row = m >> 3; row < left; row += 8)
+                            if (nt + 8 * (m & 7) < N)
+                                *(uint4*)(yt + (size_t)row * N + 8 * (m & 7)) =
+                                    *(const uint4*)(buf + row * 128 + (((m & 7) ^ (row & 7)) * 16));
+                    } else if (nt + m < N) {
+                        for (int row = 0; row < left; ++row)
+                            yt[(size_t)row * N + m] =
+                                *(const uint16_t*)(buf + row * 128 + (((m >> 3) ^ (row & 7)) * 16) + 2 * (m & 7));
+                    }
+                    __syncwarp();
                 }
             }
         }
+        if (issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     asm volatile("tcgen05.fence::before_thread_sync;");
     __syncwarp();
@@ -873,23 +898,26 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
 // ---------------------------------------------------------------------------------------
 
 struct Maps {
-    CUtensorMap w, ws, x, xs;
+    CUtensorMap w, ws, x, xs, y;
 };
 
-wq_status encode_u8(CUtensorMap* map, const void* base, int64_t row_bytes, int64_t rows, int box_bytes, int box_rows,
-                    bool swizzle, const char* what) {
+wq_status encode(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int64_t cols, int64_t rows,
+                 int box_cols, int box_rows, bool swizzle, const char* what) {
     auto enc = tensor_map_encoder();
     if (!enc) return fail(WQ_ECUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
-    cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-    cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows};
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)cols * (cuuint64_t)size};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     cuuint32_t es[2] = {1, 1};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void*)base, dims, strides, box, es,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const CUresult r = enc(map, type, 2, (void*)base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(WQ_ECUDA, "tensor map for %s failed (%d)", what, (int)r);
     return WQ_OK;
+}
+wq_status encode_u8(CUtensorMap* map, const void* base, int64_t row_bytes, int64_t rows, int box_bytes, int box_rows,
+                    bool swizzle, const char* what) {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, row_bytes, rows, box_bytes, box_rows, swizzle, what);
 }
 
 template <int BN, int CL, bool EXPERTS, bool XQ>
@@ -943,7 +971,7 @@ wq_status launch_pair(const Maps& mp, const int32_t* offsets, int experts, uint1
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = overlap ? 1 : 0;
-    cudaLaunchKernelEx(&cfg, k, mp.w, mp.ws, mp.x, mp.xs, offsets, experts, y, M, N, K, grid_n, grid_m, bn);
+    cudaLaunchKernelEx(&cfg, k, mp.w, mp.ws, mp.x, mp.xs, mp.y, offsets, experts, y, M, N, K, grid_n, grid_m, bn);
     return check_launch("mxfp4 gemm (pairs)");
 }
 
@@ -975,6 +1003,10 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
         if ((st = encode_u8(&mp.ws, wsc, pitch, n * experts, 16, BM, false, "the weight scales"))) return st;
         if ((st = encode_u8(&mp.x, xp, k / 2, m, 128, bn / 2, true, "the activation codes"))) return st;
         if ((st = encode_u8(&mp.xs, xsc, pitch, m, 16, bn, false, "the activation scales"))) return st;
+        mp.y = mp.w;                                             // not used where y's rows are not aligned
+        if (n % 8 == 0 &&
+            (st = encode(&mp.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, y, n, m, 64, 32, true, "the products")))
+            return st;
         return offsets ? launch_pair<true>(mp, offsets, experts, y, M, N, K, gn, (int)gm, bn, overlap, s)
                        : launch_pair<false>(mp, offsets, experts, y, M, N, K, gn, (int)gm, bn, overlap, s);
     }
