@@ -257,3 +257,255 @@ def test_experts_with_no_rows_at_all(wq):
     y = wq.gemm_experts_mxfp4(pw, torch.empty((0, 128), dtype=torch.bfloat16, device="cuda"),
                               torch.zeros(5, dtype=torch.int32, device="cuda"))
     assert y.shape == (0, 64)
+
+
+# --- as they are used --------------------------------------------------------------------
+
+@pytest.mark.parametrize("m, n, k", [(3, 200, 576), (40, 130, 1088), (100, 260, 512), (300, 264, 320), (260, 131, 320)])
+def test_nothing_outside_the_output_is_written(wq, m, n, k):
+    codes, scale = weights(n, k, 1)
+    pw = packed(wq, codes, scale)
+    x = acts(m, k, 2)
+    pad = 24
+    buf = torch.full((m + 2 * pad, n), 7.25, dtype=torch.bfloat16, device="cuda")
+    lo = next(r for r in range(pad) if (r * n * 2) % 16 == 0 and r > 0) if (n * 2) % 16 else pad
+    out = buf[lo:lo + m]
+    wq.gemm_mxfp4(pw, x.cuda(), out=out)
+    assert (buf[:lo] == 7.25).all() and (buf[lo + m:] == 7.25).all()
+    xc, xs = mx.quantize(x.double().numpy())
+    check(out, mx.values(xc, xs), mx.values(codes, scale))
+
+
+def test_nan_blocks_reach_their_rows_and_columns_only(wq):
+    """A NaN scale byte of x makes one row of y NaN, one of w a column; few rows (quantised by the
+    product), some, and many."""
+    n, k = 260, 576
+    codes, scale = weights(n, k, 1)
+    scale[77, 3] = 255
+    pw = packed(wq, codes, scale)
+    for m in (9, 50, 300):
+        x = acts(m, k, m)
+        x[m // 2, 100] = float("inf")
+        y = wq.gemm_mxfp4(pw, x.cuda()).float().cpu().numpy()
+        bad = np.zeros((m, n), bool)
+        bad[m // 2] = True
+        bad[:, 77] = True
+        assert np.array_equal(np.isnan(y), bad)
+
+
+@pytest.mark.parametrize("m, experts", [(5, 0), (48, 0), (300, 0), (40, 4), (700, 3)])
+def test_captured_and_replayed(wq, m, experts):
+    """One capture, replayed on new activations (and offsets), gives what eager calls give; two
+    graphs, each with buffers of its own, replayed at once on two streams, too."""
+    n, k = 256, 640
+    codes, scale = weights(max(1, experts) * n, k, 3)
+    pw = packed(wq, codes, scale)
+
+    def call(x, off, out):
+        return wq.gemm_experts_mxfp4(pw, x, off, out=out) if experts else wq.gemm_mxfp4(pw, x, out=out)
+
+    def offsets(seed):
+        cut = np.sort(np.random.default_rng(seed).integers(0, m + 1, experts - 1)) if experts else []
+        return torch.tensor([0, *cut, m], dtype=torch.int32, device="cuda")
+
+    graphs = []
+    for g in range(2):
+        x, off = acts(m, k, g).cuda(), offsets(g)
+        out = torch.zeros((m, n), dtype=torch.bfloat16, device="cuda")
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            call(x, off, out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            call(x, off, out)
+        graphs.append((graph, x, off, out, s))
+    for step in range(3):
+        want = []
+        for g, (graph, x, off, out, s) in enumerate(graphs):
+            x.copy_(acts(m, k, 10 * step + g))
+            off.copy_(offsets(10 * step + g))
+            out.zero_()
+            want.append(call(x, off, torch.zeros_like(out)))
+        torch.cuda.synchronize()
+        for graph, x, off, out, s in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (graph, x, off, out, s), w in zip(graphs, want):
+            assert torch.equal(out, w)
+    assert wq.device_error() == 0
+
+
+def test_other_streams_and_a_workspace_of_the_callers(wq):
+    """Inputs made on a side stream, the call on the same stream, no synchronisation between."""
+    n, k, m = 384, 1024, 200
+    codes, scale = weights(n, k, 3)
+    pw = packed(wq, codes, scale)
+    need = wq.gemm_mxfp4_workspace_bytes(m, k)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    outs = []
+    for i, s in enumerate(streams):
+        with torch.cuda.stream(s):
+            x = acts(m, k, i).cuda(non_blocking=True) * 1.0
+            ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+            outs.append((wq.gemm_mxfp4(pw, x, workspace=ws), ws, x))
+    torch.cuda.synchronize()
+    for i, (y, _, x) in enumerate(outs):
+        xc, xs = mx.quantize(x.double().cpu().numpy())
+        check(y, mx.values(xc, xs), mx.values(codes, scale))
+
+
+def test_calls_repeat_bit_for_bit(wq):
+    for m, n, k in [(2, 300, 8192), (20, 512, 4096), (90, 200, 4096), (500, 640, 2048)]:
+        codes, scale = weights(n, k, 3)
+        pw, x = packed(wq, codes, scale), acts(m, k, 4).cuda()
+        y = wq.gemm_mxfp4(pw, x)
+        assert all(torch.equal(y, wq.gemm_mxfp4(pw, x)) for _ in range(5))
+
+
+def test_binding_refuses_on_the_gpu(wq):
+    codes, scale = weights(64, 128, 1)
+    pw = packed(wq, codes, scale)
+    x = acts(8, 128, 1).cuda()
+    with pytest.raises(TypeError):
+        wq.gemm_mxfp4(pw, x.float())
+    with pytest.raises(TypeError):
+        wq.quantize_mxfp4(x.half())
+    with pytest.raises(ValueError):
+        wq.gemm_mxfp4(pw, x[:, :64])
+    with pytest.raises(ValueError):
+        wq.gemm_mxfp4(pw, x.t().contiguous().t())
+    with pytest.raises(ValueError):
+        wq.gemm_mxfp4(pw, x, out=torch.empty((8, 63), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(TypeError):
+        wq.gemm_mxfp4(pw, x, out=torch.empty((8, 64), device="cuda"))
+    off = torch.tensor([0, 3, 8], dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError):
+        wq.gemm_experts_mxfp4(pw, x, off.long())
+    with pytest.raises(ValueError):                      # 64 rows are no 3 experts'
+        wq.gemm_experts_mxfp4(pw, x, torch.tensor([0, 1, 2, 8], dtype=torch.int32, device="cuda"))
+    with pytest.raises(wq.WqError) as e:                 # offsets not 16-byte aligned
+        wq.gemm_experts_mxfp4(pw, x, torch.zeros(8, dtype=torch.int32, device="cuda")[1:4])
+    assert e.value.status == wq.WQ_EALIGN
+    wq.debug_fail_next_launches(1)
+    with pytest.raises(wq.WqError) as e:
+        wq.gemm_mxfp4(pw, x)
+    assert e.value.status == wq.WQ_ECUDA
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    d = pw.desc()
+    import ctypes
+    xx = acts(40, 128, 1).cuda()
+    y = torch.empty((40, 64), dtype=torch.bfloat16, device="cuda")
+    assert wq._lib.wq_gemm_mxfp4_bf16(ctypes.byref(d), xx.data_ptr(), 40, y.data_ptr(), small.data_ptr(), 16,
+                                      None) == wq.WQ_EINVAL and "workspace" in wq.last_error()
+
+
+def test_an_output_past_two_to_the_31_elements(wq):
+    """y[m, n] of 2.2 G elements: rows at its start, its middle and its end, exactly (one-hot x)."""
+    m, n, k = 67000, 32832, 64
+    codes, scale = weights(n, k, 8)
+    x, at = one_hot(m, k, 5)
+    y = wq.gemm_mxfp4(packed(wq, codes, scale), x.cuda())
+    v = mx.values(codes, scale)
+    for r in (0, 1, 33000, 65407, 65408, 66815, m - 1):
+        assert np.array_equal(f32(y[r]), v[:, at[r]]), r
+    assert wq.device_error() == 0
+
+
+def test_quantisation_past_two_to_the_35_elements(wq):
+    """Chunk numbers that need 64 bits (70 GB of activations, checked at their end)."""
+    n, k = 1 << 20, 32800
+    if torch.cuda.mem_get_info()[0] < 110 << 30:
+        pytest.skip("needs 110 GB of free memory")
+    x = torch.empty((n, k), dtype=torch.bfloat16, device="cuda")
+    rows = [0, 500_000, n - 2, n - 1]
+    for i, r in enumerate(rows):
+        x[r] = acts(1, k, i)[0].cuda()
+    pw, _ = wq.quantize_mxfp4(x)
+    for i, r in enumerate(rows):
+        codes, scale = mx.quantize(acts(1, k, i).double().numpy())
+        assert np.array_equal(pw.aux[r].cpu().numpy(), scale[0])
+        assert np.array_equal(pw.packed[r].cpu().numpy(), codes[0, 0::2] | codes[0, 1::2] << 4)
+    del x, pw
+    torch.cuda.empty_cache()
+
+
+# --- together ----------------------------------------------------------------------------
+
+def test_a_mixture_of_experts_layer(wq):
+    """Coded projections and experts in a row, each against 64 bits on the inputs it was given: a
+    router's top choice sorts the rows, up and gate (stacked) by expert, SwiGLU, down by expert,
+    rows back in place, a dense projection behind; then one row of it by the W4A16 GEMV."""
+    hidden, inner, e, t = 256, 448, 6, 75
+    g = torch.Generator().manual_seed(3)
+
+    def coded(rows, cols):
+        w = (torch.randn((rows, cols), generator=g) * 0.1).bfloat16()
+        codes, scale = mx.quantize(w.double().numpy())
+        pw, _ = wq.quantize_mxfp4(w.cuda())
+        assert np.array_equal(pw.aux.cpu().numpy(), scale)
+        return pw, mx.values(codes, scale)
+
+    up, upv = coded(e * 2 * inner, hidden)
+    down, downv = coded(e * hidden, inner)
+    head, headv = coded(320, hidden)
+    x = torch.randn((t, hidden), generator=g).bfloat16().cuda()
+    expert = (x @ torch.randn((hidden, e), generator=g).bfloat16().cuda()).argmax(1)
+    order = expert.argsort(stable=True)
+    off = torch.cat([torch.zeros(1, device="cuda", dtype=torch.int64), torch.bincount(expert, minlength=e).cumsum(0)]).int()
+    xs = x[order].contiguous()
+    a = wq.gemm_experts_mxfp4(up, xs, off)
+    act = (torch.nn.functional.silu(a[:, :inner].float()) * a[:, inner:].float()).bfloat16()
+    b = wq.gemm_experts_mxfp4(down, act, off)
+    back = torch.empty_like(b)
+    back[order] = b
+    y = wq.gemm_mxfp4(head, back)
+    one = wq.gemv(head, back[:1].contiguous())
+    torch.cuda.synchronize()
+    offs = off.cpu().numpy()
+
+    def coded_rows(v):
+        return mx.values(*mx.quantize(v.double().cpu().numpy()))
+
+    for got, rows, wv, n in ((a, xs, upv, 2 * inner), (b, act, downv, hidden)):
+        ref, bound = experts_ref(coded_rows(rows), wv, offs, n)
+        assert (np.abs(f32(got) - ref) <= matmul_tolerance(ref, bound)).all()
+    check(y, coded_rows(back), headv)
+    check(one, back[:1].double().cpu().numpy(), headv)
+
+
+def test_fake_quantisation_in_a_training_step(wq):
+    """Straight through: the forward value is the code value, the gradient reaches the latents as
+    it is. Against the formula, and against differences of the loss in the code values."""
+    class Straight(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, z):
+            return wq.fake_quant_mxfp4(z.detach())[0]
+
+        @staticmethod
+        def backward(ctx, g):
+            return g
+
+    g = torch.Generator().manual_seed(1)
+    z = torch.randn((24, 96), generator=g).cuda().requires_grad_()
+    x = torch.randn((10, 96), generator=g).double().cuda()
+    q = Straight.apply(z)
+    codes, scale = mx.quantize(z.detach().double().cpu().numpy())
+    v = mx.values(codes, scale)
+    assert np.array_equal(q.detach().double().cpu().numpy(), v)
+    loss = ((x @ q.double().T) ** 2).sum()
+    loss.backward()
+    xn = x.cpu().numpy()
+    want = 2 * (v @ xn.T) @ xn
+    got = z.grad.double().cpu().numpy()
+    # the gradient is rounded to fp32 once
+    assert (np.abs(got - want) <= 2.0 ** -23 * np.abs(want) + 1e-300).all()
+    d = 1e-3
+    for i, j in ((0, 0), (7, 50), (23, 95)):
+        e = np.zeros_like(v)
+        e[i, j] = d
+        diff = (((xn @ (v + e).T) ** 2).sum() - ((xn @ (v - e).T) ** 2).sum()) / (2 * d)
+        assert abs(diff - got[i, j]) <= 1e-6 * (np.abs(want).max() + 1)

@@ -144,6 +144,11 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
+def _matrix(rows: int, cols: int, dtype, device) -> torch.Tensor:
+    """An uninitialised row-major matrix (torch.empty, for less host time a call)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
 def _cuda(t: torch.Tensor, dtype, name: str) -> torch.Tensor:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
@@ -262,10 +267,9 @@ def _quantize_mx(x: torch.Tensor, codes: bool, packed: bool, q: bool):
         raise ValueError("x must be a contiguous [n, k] matrix")
     n, k = x.shape
     dev = x.device
-    u8 = torch.uint8
-    s = torch.empty((n, mx_pitch(k)), dtype=u8, device=dev) if packed or codes else None
-    c = torch.empty((n, k), dtype=u8, device=dev) if codes else None
-    p = torch.empty((n, k // 2), dtype=u8, device=dev) if packed else None
+    s = _matrix(n, mx_pitch(k), torch.uint8, dev) if packed or codes else None
+    c = _matrix(n, k, torch.uint8, dev) if codes else None
+    p = _matrix(n, k // 2, torch.uint8, dev) if packed else None
     v = torch.empty_like(x) if q else None
     _check(_lib.wq_quantize_mxfp4(_ptr(x), F32 if x.dtype == torch.float32 else BF16, n, k, _ptr(s), _ptr(c),
                                   _ptr(p), _ptr(v), _stream(x)))
@@ -329,7 +333,7 @@ def gemv(w: PackedWeight, x: torch.Tensor, out: torch.Tensor | None = None) -> t
     x2 = x if x.dim() == 2 else x.reshape(1, -1)
     _cuda(x2, torch.bfloat16, "x")
     b = x2.shape[0]
-    y = out if out is not None else torch.empty((b, w.n), dtype=torch.bfloat16, device=x2.device)
+    y = out if out is not None else _matrix(b, w.n, torch.bfloat16, x2.device)
     d = w.desc()
     _check(_lib.wq_gemv_w4a16(ctypes.byref(d), _ptr(x2), b, _ptr(y), _stream(x2)))
     if host:
@@ -458,7 +462,7 @@ def _mx_product(w: PackedWeight, x, out, workspace, offsets):
     if k != w.k:
         raise ValueError(f"x has {k} columns, w has {w.k}")
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=t.device) if coded else x.new_empty((m, n))
+        out = _matrix(m, n, torch.bfloat16, t.device)
     else:
         _cuda(out, torch.bfloat16, "out")
         if tuple(out.shape) != (m, n):

@@ -24,6 +24,7 @@
 // (see wq_device_error) and the CTA skips the rest of its work, still releasing its tensor
 // memory.
 #include <algorithm>
+#include <atomic>
 
 #include "wq_tcgen05.cuh"
 
@@ -920,14 +921,25 @@ wq_status encode_u8(CUtensorMap* map, const void* base, int64_t row_bytes, int64
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, row_bytes, rows, box_bytes, box_rows, swizzle, what);
 }
 
+// Opts the kernel in to `bytes` of shared memory on the current device, once for each device
+// (`raised`: one bit a device, per kernel).
+template <typename Kernel>
+void raise_smem(Kernel k, int bytes, std::atomic<uint64_t>& raised) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev > 63) dev = 63;
+    const uint64_t bit = (uint64_t)1 << dev;
+    if ((raised.load(std::memory_order_relaxed) & bit) && dev != 63) return;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess)
+        raised.fetch_or(bit, std::memory_order_relaxed);
+}
+
 template <int BN, int CL, bool EXPERTS, bool XQ>
 wq_status launch_one(const Maps& mp, const uint16_t* x16, const int32_t* offsets, int experts, uint16_t* y, int M, int N, int K,
                      int grid_n, int64_t grid_m, int kt_per_split, bool overlap, cudaStream_t s) {
     auto k = mx_gemm_kernel<BN, CL, EXPERTS, XQ>;
     constexpr int smem = Cfg<BN>::TOTAL;
-    static bool raised = false;        // the shared-memory opt-in holds for the process
-    if (!raised && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess)
-        raised = true;
+    static std::atomic<uint64_t> raised{0};
+    raise_smem(k, smem, raised);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(grid_n * grid_m), CL, 1);
     cfg.blockDim = dim3(kThreads);
@@ -957,9 +969,8 @@ template <bool EXPERTS>
 wq_status launch_pair(const Maps& mp, const int32_t* offsets, int experts, uint16_t* y, int M, int N, int K,
                       int grid_n, int grid_m, int bn, bool overlap, cudaStream_t s) {
     auto k = mx_gemm_pair_kernel<EXPERTS>;
-    static bool raised = false;
-    if (!raised && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Pair::TOTAL) == cudaSuccess)
-        raised = true;
+    static std::atomic<uint64_t> raised{0};
+    raise_smem(k, Pair::TOTAL, raised);
     cudaLaunchConfig_t cfg = {};
     const int64_t tiles = (int64_t)grid_n * grid_m;
     cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, sm_count() / 2)), 1, 1);
