@@ -536,7 +536,11 @@ __device__ __forceinline__ bool stage_x(uint8_t* xs, const uint16_t* x, int B, i
 // Steps of weight bytes held in registers per warp (D - 1 of them in flight): the bytes in
 // flight per SM, warps x (D - 1) x 2 KB, set the bandwidth a latency-bound stream reaches,
 // and deeper buffers buy them at fewer registers than more warps would.
+// (MXFP4: three steps and 16 warps an SM, 8192 x 28672 at batch 1: 38.2 us; two and 20: 41.0; four
+// and 16: 39.9; three and 20, which spills: 48.5. Copied through shared memory by cp.async, four
+// steps deep and 24 warps: 50.)
 constexpr int depth(int kind, int nb, int r) {
+    if (kind == kMx4 && nb == 1 && r == 1) return 3;
     return (kind < kLut16 && nb == 1 && r == 1) ? WQ_GEMV_DEPTH : 2;
 }
 
@@ -578,7 +582,8 @@ constexpr int cta_warps(int wk, int fw) { return wk == 1 ? fw : 4; }
 #define WQ_GEMV_LLOYD_CAP 1
 #endif
 constexpr int min_warps(int kind, int nb, int r, int warps_per_cta) {
-    return kind == kLloyd8 ? 4 * WQ_GEMV_LLOYD_CAP
+    return kind == kMx4 && nb == 1 ? 16
+         : kind == kLloyd8 ? 4 * WQ_GEMV_LLOYD_CAP
          : kind == kLut16 ? 4 * WQ_GEMV_LUT_CAP
          : r != 1 ? 4 * WQ_GEMV_R2_CAP
          : nb != 1 ? 4 * WQ_GEMV_MIN_CTAS_NB2
