@@ -965,6 +965,22 @@ wq_status launch_one(const Maps& mp, const uint16_t* x16, const int32_t* offsets
     return check_launch("mxfp4 gemm");
 }
 
+// Activation rows a tile of the pair kernel: the grid runs in rounds of `pairs` tiles, a tile takes
+// a time of about bn + 400 (an MMA reads its 256 weight rows, and takes 128 clocks, whatever bn;
+// the way out, and the tile's fill, grow with it), and the fewest rounds times that wins. `rows`: of
+// one expert; `columns`: weight tiles of all. Measured at 4096 x 4096 weights: 256 rows 11.3 us in
+// 16 tiles of 256, 8.6 in 64 of 64; 512 rows 11.7 in 32 of 256, 9.8 in 64 of 128; 1024 rows 12.1 in
+// 64 of 256, 14.0 in 128 of 128; 512 rows of 11008 x 4096 17.5 / 15.8 / 18.6 at 256 / 192 / 128.
+int pair_width(int64_t rows, int64_t columns, int64_t pairs) {
+    int best = 256;
+    int64_t least = -1;
+    for (int bn = 256; bn >= 32; bn -= 16) {
+        const int64_t tiles = columns * ((rows + bn - 1) / bn), cost = (tiles + pairs - 1) / pairs * (bn + 400);
+        if (least < 0 || cost < least) { least = cost; best = bn; }
+    }
+    return best;
+}
+
 template <bool EXPERTS>
 wq_status launch_pair(const Maps& mp, const int32_t* offsets, int experts, uint16_t* y, int M, int N, int K,
                       int grid_n, int grid_m, int bn, bool overlap, cudaStream_t s) {
@@ -1004,10 +1020,7 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
     wq_status st;
     if (rows > 128) {
         const int gn = (N + 255) / 256;
-        // as few activation tiles as hold all rows, of equal width: a stage of 256 columns takes 617
-        // clocks at 256 rows and still 505 at 64 (16384 columns, per pair)
-        const int64_t wide = (m + 255) / 256;
-        const int bn = offsets ? 256 : (int)((m + 16 * wide - 1) / (16 * wide)) * 16;
+        const int bn = pair_width(rows, (int64_t)gn * experts, sms / 2);
         const int64_t gm = offsets ? m / bn + std::min<int64_t>(experts, m) : (m + bn - 1) / bn;
         if (gm * gn > 0x3FFFFFFF) return fail(WQ_EUNSUPPORTED, "more than 2^30 - 1 tiles");
         if ((st = encode_u8(&mp.w, wp, k / 2, n * experts, KB / 2, BM, true, "the weight codes"))) return st;
