@@ -172,7 +172,8 @@ typedef enum wq_dtype {
  *   q       out [n, k] of the same dtype: level * 2^(s - 127), exact in both types (the
  *           forward value of fake quantisation; its straight-through backward is the
  *           identity and needs no call), or NULL.
- * At least one of codes, packed and q must be non-NULL. Bit-exact (NaNs of q: any NaN). */
+ * At least one of codes, packed and q must be non-NULL; no output may overlap x. Bit-exact
+ * (NaNs of q: any NaN). */
 wq_status wq_quantize_mxfp4(const void* x, int32_t dtype, int64_t n, int64_t k, uint8_t* scale,
                             uint8_t* codes, uint8_t* packed, void* q, wq_stream stream);
 
@@ -350,7 +351,8 @@ wq_status wq_gemm_mxfp4(const wq_weight* w, const wq_weight* x, uint16_t* y, wq_
  * product's own kernel for few rows, else first, into the workspace (m < 2^30). The two kernels
  * then overlap: the product starts while the activations are quantised.
  *   ws  device workspace of at least wq_gemm_mxfp4_workspace_bytes(m, k, 0) bytes (NULL if 0;
- *       the grouped form below: with its number of experts). */
+ *       the grouped form below: with its number of experts). Calls that may overlap on the
+ *       GPU need a workspace each. */
 wq_status wq_gemm_mxfp4_bf16(const wq_weight* w, const uint16_t* x, int64_t m, uint16_t* y,
                              void* ws, size_t ws_bytes, wq_stream stream);
 
@@ -358,7 +360,7 @@ wq_status wq_gemm_mxfp4_bf16(const wq_weight* w, const uint16_t* x, int64_t m, u
  * expert, rows offsets[e] .. offsets[e + 1] - 1 belong to expert e, and
  * y[i, r] = sum_c Wdeq[e n + r, c] * Xdeq[i, c] for those rows.
  *   w        the experts' weights stacked: MXFP4 [experts * n, k] (w->n = experts * n).
- *   experts  1 .. 65536, a divisor of w->n.
+ *   experts  1 .. 4096, a divisor of w->n.
  *   offsets  DEVICE int32 [experts + 1], non-decreasing, 0 <= offsets[0],
  *            offsets[experts] <= m. Read on the device only. Experts may have no rows; rows
  *            before offsets[0] and from offsets[experts] on belong to no expert, and their

@@ -108,7 +108,7 @@ def test_dequant_at_the_ends_of_the_scales(wq):
     scale[:, 0] = np.arange(256)
     v = mx.values(codes, scale)
     d = wq.dequant(packed(wq, codes, scale)).cpu().double().numpy()
-    v = np.where(np.abs(v) >= 2.0 ** 128, np.sign(v) * np.inf, v)      # past bf16's largest
+    v = np.where(np.abs(v) >= 2.0 ** 128, np.copysign(np.inf, v), v)   # past bf16's largest
     assert np.array_equal(d, v, equal_nan=True)
 
 
@@ -157,6 +157,15 @@ def test_gemv_grouped_and_plan(wq):
     for y, r in zip(ys, refs):
         check(y, *r)
     plan.close()
+
+
+@pytest.mark.parametrize("m", [40, 200])
+def test_gemm_static(wq, m):
+    """The GEMM on the library's own scratch takes the format, too."""
+    n, k = 512, 4096
+    codes, scale = weights(n, k, 5)
+    x = acts(m, k, m)
+    check(wq.gemm_static(packed(wq, codes, scale), x.cuda()), x.double().numpy(), mx.values(codes, scale))
 
 
 # --- block-scaled products ---------------------------------------------------------------
@@ -216,6 +225,7 @@ def experts_ref(xv, wv, off, n):
     ([1], 128, 64), ([3], 100, 512), ([0, 1], 7, 64), ([1, 0, 0, 2], 130, 576), ([0, 0, 5, 0], 257, 128),
     ([16, 17, 1, 0, 15, 33], 200, 1088), ([130, 0, 1, 257, 64], 300, 192), ([500, 3], 129, 1024),
     ([1] * 70, 64, 256), ([0] * 40 + [2] + [0] * 30 + [9], 33, 320), ([300, 0, 290, 310], 384, 512),
+    ([0, 3, 0] * 100 + [40] + [1] * 33, 16, 64), ([0] * 500 + [5] + [0] * 523, 8, 64), ([200] * 40, 24, 64),
 ])
 def test_experts(wq, counts, n, k):
     e, t = len(counts), sum(counts)

@@ -50,7 +50,7 @@ def test_product_refusals(wq, host):
     assert lib.wq_gemm_mxfp4(by(odd), by(odd), p, None) == wq.WQ_EINVAL
     assert lib.wq_gemm_mxfp4(by(good), by(good), p, None) == wq.WQ_EINVAL            # host memory
     assert lib.wq_gemm_mxfp4_bf16(by(good), p, 0, p, p, 1 << 20, None) == wq.WQ_EINVAL
-    for e in (0, -1, 65537):
+    for e in (0, -1, 4097):
         assert lib.wq_gemm_mxfp4_experts(by(good), e, p, by(good), p, None) == wq.WQ_EINVAL
         assert "experts" in wq.last_error() or "device memory" in wq.last_error() or "Attributes" in wq.last_error()
         assert lib.wq_gemm_mxfp4_experts_bf16(by(good), e, p, p, 3, p, p, 1 << 20, None) == wq.WQ_EINVAL
@@ -79,6 +79,12 @@ def test_binding_refusals(wq):
         wq.gemm_mxfp4(w, x)
     with pytest.raises(ValueError):
         wq.gemm_mxfp4(wq.PackedWeight(wq.FMT_DYADIC4, 32, 8, 64, z, z), w)
+    # scale bytes without the rows' padding
+    with pytest.raises(ValueError):
+        wq.PackedWeight(wq.FMT_MXFP4, 32, 8, 64, torch.zeros((8, 32), dtype=torch.uint8),
+                        torch.zeros((8, 2), dtype=torch.uint8)).desc()
+    wq.PackedWeight(wq.FMT_MXFP4, 32, 8, 64, torch.zeros((8, 32), dtype=torch.uint8),
+                    torch.zeros((8, 16), dtype=torch.uint8)).desc()
     with pytest.raises(ValueError):
         wq.gemm_mxfp4(w, wq.PackedWeight(wq.FMT_MXFP4, 32, 4, 128, z, z))
     with pytest.raises(ValueError):

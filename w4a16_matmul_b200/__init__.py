@@ -176,6 +176,10 @@ class PackedWeight:
                                   # MXFP4: uint8 [n, mx_pitch(k)], k/32 scale bytes a row
 
     def desc(self) -> WqWeight:
+        if self.fmt == FMT_MXFP4 and (self.packed.numel() * 2 != self.n * self.k or
+                                      self.aux.numel() != self.n * ((self.k + 511) // 512 * 16) or
+                                      not (self.packed.is_contiguous() and self.aux.is_contiguous())):
+            raise ValueError("an MXFP4 weight holds contiguous packed [n, k/2] and scale bytes [n, mx_pitch(k)]")
         return WqWeight(self.fmt, self.group, self.n, self.k, self.packed.data_ptr(), self.aux.data_ptr())
 
 

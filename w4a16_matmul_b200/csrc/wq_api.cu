@@ -166,7 +166,7 @@ const char* wq_status_string(int32_t s) {
 
 const char* wq_last_error(void) { return g_last_error; }
 
-int32_t wq_version(void) { return 100; }
+int32_t wq_version(void) { return 200; }
 
 void wq_debug_fail_next_launches(int32_t count) { g_fail_next.store(count > 0 ? count : 0); }
 
@@ -570,7 +570,7 @@ wq_status check_mx_product(const wq_weight* w, int32_t experts, const int32_t* o
     wq_status st = check_mx(w, "w");
     if (st) return st;
     if (experts != 0) {
-        if (experts < 1 || experts > 65536) return fail(WQ_EINVAL, "experts=%d outside 1..65536", experts);
+        if (experts < 1 || experts > 4096) return fail(WQ_EINVAL, "experts=%d outside 1..4096", experts);
         if (w->n % experts != 0)
             return fail(WQ_EINVAL, "the stack's %lld rows are not a multiple of %d experts", (long long)w->n, experts);
         if ((st = check_ptr(offsets, "offsets", false))) return st;
@@ -638,13 +638,13 @@ wq_status wq_gemm_mxfp4_bf16(const wq_weight* w, const uint16_t* x, int64_t m, u
 
 wq_status wq_gemm_mxfp4_experts(const wq_weight* w, int32_t experts, const int32_t* offsets, const wq_weight* x,
                                 uint16_t* y, wq_stream stream) {
-    if (experts == 0) { g_last_error[0] = 0; return fail(WQ_EINVAL, "experts=0 outside 1..65536"); }
+    if (experts == 0) { g_last_error[0] = 0; return fail(WQ_EINVAL, "experts=0 outside 1..4096"); }
     return mx_product(w, experts, offsets, x, y, (cudaStream_t)stream);
 }
 
 wq_status wq_gemm_mxfp4_experts_bf16(const wq_weight* w, int32_t experts, const int32_t* offsets, const uint16_t* x,
                                      int64_t m, uint16_t* y, void* ws, size_t ws_bytes, wq_stream stream) {
-    if (experts == 0) { g_last_error[0] = 0; return fail(WQ_EINVAL, "experts=0 outside 1..65536"); }
+    if (experts == 0) { g_last_error[0] = 0; return fail(WQ_EINVAL, "experts=0 outside 1..4096"); }
     return mx_product_bf16(w, experts, offsets, x, m, y, ws, ws_bytes, (cudaStream_t)stream);
 }
 

@@ -1,5 +1,6 @@
 // wq_dyadic.cu -- dyadic 4-bit quantisation ("MiniCPM5-1B 验证: 6× 压缩…" §2.1-2.3),
-// nibble pack / unpack (§2.5) and dense reconstruction of all three packed formats.
+// nibble pack / unpack (§2.5) and dense reconstruction of the three codebook formats (MXFP4's
+// is in wq_mx.cu).
 //
 // All four kernels are HBM-bound streams: one thread owns a 16-byte chunk of the widest
 // array it touches, loads are 128-bit and coalesced, grids are a multiple of the SM count

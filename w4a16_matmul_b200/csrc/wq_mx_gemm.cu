@@ -11,9 +11,12 @@
 //              bytes] and of the activation tile [BN x 128 bytes], 128-byte swizzle; per 512
 //              columns the scale bytes of both [128 + BN rows x 16 bytes];
 //   warp 1     allocates tensor memory, and one lane issues the MMAs (K = 64 each);
-//   warps 2-5  (few rows: quantise the activations; see XQ below) move the scale bytes into tensor memory: the MMA wants the four bytes of row r's
+//   warps 2-5  move the scale bytes into tensor memory: the MMA wants the four bytes of row r's
 //              128 columns in lane r % 32 of column r / 32, in each of the four lane quarters,
-//              so each warp fills its own quarter; afterwards they drain the accumulator.
+//              so each warp fills its own quarter; afterwards they drain the accumulator. For few
+//              rows they quantise the activations, too (XQ below).
+// Up to 128 activation rows (of an expert, on average) run this way; more run on pairs of CTAs,
+// the second kernel below.
 // Grouped by expert, a CTA finds its expert and its rows from the offsets on the device: the
 // host reads nothing back, and launches as many row tiles as the worst distribution needs.
 // Rows of the activation tile past the expert's range belong to the next expert (or lie behind
@@ -139,6 +142,34 @@ __device__ __forceinline__ MxTile find_tile(const int32_t* __restrict__ offsets,
     return MxTile{-1, 0, 0};
 }
 
+// Moves `at` to the group of consecutive experts, one of 32, that holds row tile `mt`: every lane
+// adds up the tiles of its group, its loads independent of one another, where the walk would meet
+// the memory's latency once every 32 experts.
+__device__ __forceinline__ void skip_experts(const int32_t* __restrict__ offsets, int experts, int M, int mt, int bn,
+                                             MxScan& at) {
+    const int lane = threadIdx.x & 31, group = (experts + 31) / 32;
+    const int e0 = min(experts, lane * group), e1 = min(experts, e0 + group);
+    int tiles = 0;
+#pragma unroll 8
+    for (int e = e0; e < e1; ++e) {
+        const int lo = min(max(__ldg(offsets + e), 0), M), hi = min(max(__ldg(offsets + e + 1), lo), M);
+        tiles += (hi - lo + bn - 1) / bn;
+    }
+    int incl = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    const int f = __ffs(__ballot_sync(0xFFFFFFFFu, incl > mt)) - 1;
+    if (f < 0) {                                                 // there is no such tile
+        at.e0 = experts;
+        return;
+    }
+    at.e0 = f * group;
+    at.before = __shfl_sync(0xFFFFFFFFu, incl - tiles, f);
+}
+
 // Activations as they come, for tiles of at most 32 rows (XQ): warps 2-5 quantise them on the way
 // into the stage, a block of 32 columns a thread at a time, one scale stage ahead in registers.
 // Every CTA of a row tile repeats that work, which few rows make cheap; it saves the kernel in
@@ -240,6 +271,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     if (EXPERTS) {
         if (warp == 0) {
             MxScan at;
+            // (64 experts, 25 with rows: 11.8 us by the walk alone, 13.4 with this in front)
+            if (experts > 64) skip_experts(offsets, experts, M, lin / grid_n, BN, at);
             tile = find_tile(offsets, experts, M, lin / grid_n, BN, at);
             if (lane == 0) { s_tile[0] = tile.expert; s_tile[1] = tile.t0; s_tile[2] = tile.tend; }
         }
@@ -496,9 +529,11 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 // Many activation rows: pairs of CTAs (cta_group::2) on tiles of 256 weight rows x bn <= 256
 // activation rows, walked by a persistent grid. Each CTA of a pair holds half of the weight
 // rows and half of the activation rows in shared memory and accumulates its 128 weight rows x
-// bn: per MMA it reads 128 + bn / 2 rows where a single CTA reads 128 + bn. Shared memory is
-// what bounds the 4-bit product: at 128 x 256 the MMA's reads and the TMA's writes are 192
-// bytes a clock against 128 (measured 834 clocks a stage of 256 columns; the MMAs take 512).
+// bn: per MMA of 64 columns it reads (128 + bn / 2) x 32 bytes where a single CTA reads (128 + bn)
+// x 32. At 256 x 256 that is 64 bytes a clock, and the copies into shared memory take as many
+// again, of the 128 there are; a single CTA's 128 x 256 tile would want 192. The MMAs bound the
+// kernel: 131 clocks each (128 by their rate), measured 0.31 us a stage of four at 1.9 GHz; 5.5
+// PFLOP/s over 4096 x 4096 x 11008, at the power limit.
 //   warp 0      TMA producer of its CTA's codes (both CTAs signal the leader's barrier);
 //   warp 1      MMA issuer (the leader's CTA only), commits to both CTAs;
 //   warps 2-5   scale bytes into tensor memory: the CTA's 128 weight rows and all activation rows;
