@@ -416,11 +416,11 @@ def gemm(w: PackedWeight, x: torch.Tensor, out: torch.Tensor | None = None,
     """y = x Wdeq^T for x bf16 [m, k] -> bf16 [m, n] on the tcgen05 tensor cores."""
     _cuda(x, torch.bfloat16, "x")
     m = x.shape[0]
-    y = out if out is not None else torch.empty((m, w.n), dtype=torch.bfloat16, device=x.device)
-    need = gemm_workspace_bytes(w, m)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    y = out if out is not None else _matrix(m, w.n, torch.bfloat16, x.device)
     d = w.desc()
+    need = int(_lib.wq_gemm_workspace_bytes(ctypes.byref(d), m))
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = _matrix(1, need, torch.uint8, x.device)
     _check(_lib.wq_gemm_w4a16(ctypes.byref(d), _ptr(x), m, _ptr(y), _ptr(workspace),
                               need, _stream(x)))
     return y
@@ -484,7 +484,7 @@ def _mx_product(w: PackedWeight, x, out, workspace, offsets):
         return out
     need = gemm_mxfp4_workspace_bytes(m, k, experts)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = x.new_empty((need + 1) // 2)
+        workspace = _matrix(1, need, torch.uint8, x.device)
     if experts:
         _check(_lib.wq_gemm_mxfp4_experts_bf16(ctypes.byref(d), experts, _ptr(offsets), _ptr(x), m, _ptr(out),
                                                _ptr(workspace), need, _stream(t)))
