@@ -313,7 +313,7 @@ size_t wq_gemm_workspace_bytes(const wq_weight* w, int64_t m);
 /* Prefill-side W4A16 GEMM on the tcgen05 tensor cores ([KM] §4.1 large batch; [DG] §3.2
  * "materialized" bf16 path fused): y[i, r] = sum_c Wdeq[r, c] * x[i, c] for i < m, fp32
  * accumulation in tensor memory, bf16 output. Formats DYADIC4 (group 64 or 32), LLOYD8S
- * (the 8-level codebook plus sign of [G32] §5.2, rebuilt per stage from the group's levels)
+ * (the 8-level codebook plus sign of [G32] §5.2, rebuilt per stage from the group's levels),
  * MXFP4 (the E2M1 level times the group's power of two, rebuilt per stage)
  * and LUT16 (the per-block-64 centroid table of [KM] §2.2, looked up per stage; the product
  * runs in fp16 on the activations converted into the workspace as x * 2^e per activation
@@ -368,7 +368,7 @@ wq_status wq_gemm_mxfp4_bf16(const wq_weight* w, const uint16_t* x, int64_t m, u
  *            overlapping ones give unspecified rows of y (never an access outside the buffers).
  *   x        as for wq_gemm_mxfp4 (or _bf16): m rows.
  *   y        out bf16 [m, n].
- * Same tolerance as wq_gemm_mxfp4. The result of a row does not depend on the other rows. */
+ * Same tolerance as wq_gemm_mxfp4. The result of a row does not depend on the other rows' values. */
 wq_status wq_gemm_mxfp4_experts(const wq_weight* w, int32_t experts, const int32_t* offsets,
                                 const wq_weight* x, uint16_t* y, wq_stream stream);
 wq_status wq_gemm_mxfp4_experts_bf16(const wq_weight* w, int32_t experts, const int32_t* offsets,
@@ -378,8 +378,8 @@ wq_status wq_gemm_mxfp4_experts_bf16(const wq_weight* w, int32_t experts, const 
 /* Reads and clears the library's device-side error words. Kernels that wait on the GPU
  * (the GEMM pipeline's mbarrier waits, the water-filled GEMV's waits for its staged bytes, the
  * MXFP4 products' pipeline waits) give up after a bounded time instead of hanging and record
- * a nonzero code (the GEMV's is 2100, the MXFP4 products' 2201 to 2206); the BF16X kernels record one when an overflow-table index would pass
- * ovf_bytes, and the water-filling kernels one when a block's width is outside 3..5 or its
+ * a nonzero code (the GEMV's is 2100, the MXFP4 products' 2201 to 2217); the BF16X kernels
+ * record one when an overflow-table index would pass ovf_bytes, and the water-filling kernels one when a block's width is outside 3..5 or its
  * bytes do not fit packed_bytes (2000 dequant, 2001 pack, 2002 GEMV; the access is skipped
  * in every case). *code receives the code (0 = none). Synchronous (copies three ints from
  * the device). Returns WQ_ETIMEOUT if a wait had expired, WQ_EDATA for inconsistent BF16X

@@ -159,6 +159,29 @@ def test_gemv_grouped_and_plan(wq):
     plan.close()
 
 
+def test_overlapped_plans_behind_a_quantisation_of_their_weights(wq):
+    """The kernel just before the last plan does not write its weights, the one before that does."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = [torch.randn((8192, 8192), generator=g, device="cuda").bfloat16() for _ in range(2)]
+    x = torch.randn((1, 8192), generator=g, device="cuda").bfloat16()
+    want = [wq.gemv(wq.quantize_mxfp4(v)[0], x) for v in w]
+    pw, _ = wq.quantize_mxfp4(w[0])
+    small, _ = wq.quantize_mxfp4(w[0][:64])
+    plans, ys = [], []
+    for p in (small, pw):
+        ys.append(torch.empty((1, p.n), dtype=torch.bfloat16, device="cuda"))
+        plans.append(wq.GroupedGemv([p], [x], [ys[-1]], overlap=True))
+    s = torch.cuda.current_stream().cuda_stream
+    for i in (1, 0, 1, 0):
+        wq._check(wq._lib.wq_quantize_mxfp4(w[i].data_ptr(), wq.BF16, 8192, 8192, pw.aux.data_ptr(), None,
+                                            pw.packed.data_ptr(), None, s))
+        for p in plans:
+            p()
+        assert torch.equal(ys[1], want[i])
+    for p in plans:
+        p.close()
+
+
 @pytest.mark.parametrize("m", [40, 200])
 def test_gemm_static(wq, m):
     """The GEMM on the library's own scratch takes the format, too."""
@@ -284,6 +307,24 @@ def test_nothing_outside_the_output_is_written(wq, m, n, k):
     assert (buf[:lo] == 7.25).all() and (buf[lo + m:] == 7.25).all()
     xc, xs = mx.quantize(x.double().numpy())
     check(out, mx.values(xc, xs), mx.values(codes, scale))
+
+
+@pytest.mark.parametrize("n", [121, 250, 251, 252, 253, 254, 255, 256, 257, 319, 321])
+def test_rows_of_every_alignment_in_wide_tiles(wq, n):
+    """Rows of y that begin at any multiple of two bytes, last rows of an expert inside a tile of 32."""
+    k, off = 320, np.array([1, 301, 302, 302, 595], np.int32)
+    codes, scale = weights(4 * n, k, n)
+    x = acts(600, k, 3)
+    xc, xs = mx.quantize(x.double().numpy())
+    out = torch.full((600, n), 7.25, dtype=torch.bfloat16, device="cuda")
+    wq.gemm_experts_mxfp4(packed(wq, codes, scale), x.cuda(), to_dev(off), out=out)
+    assert (out[:1] == 7.25).all() and (out[595:] == 7.25).all()
+    ref, bound = experts_ref(mx.values(xc, xs), mx.values(codes, scale), off, n)
+    r = slice(1, 595)
+    assert (np.abs(f32(out) - ref)[r] <= matmul_tolerance(ref, bound)[r]).all()
+    y = wq.gemm_mxfp4(packed(wq, codes[:n], scale[:n]), x.cuda())
+    check(y, mx.values(xc, xs), mx.values(codes[:n], scale[:n]))
+    assert wq.device_error() == 0
 
 
 def test_nan_blocks_reach_their_rows_and_columns_only(wq):

@@ -392,7 +392,7 @@ wq_status wq_quantize_mxfp4(const void* x, int32_t dtype, int64_t n, int64_t k, 
     if ((st = check_ptr(q, "q", true))) return st;
     if (!codes && !packed && !q) return fail(WQ_EINVAL, "codes, packed and q are all NULL");
     if ((st = check_injected())) return st;
-    return launch_quantize_mxfp4(x, dtype, n, k, scale, codes, packed, q, (cudaStream_t)stream);
+    return launch_quantize_mxfp4(x, dtype, n, k, scale, codes, packed, q, false, (cudaStream_t)stream);
 }
 
 wq_status wq_pack(const uint8_t* codes, int64_t n, int64_t k, uint8_t* packed, wq_stream stream) {
@@ -613,7 +613,7 @@ wq_status mx_product_bf16(const wq_weight* w, int32_t experts, const int32_t* of
         return launch_gemm_mxfp4(w->packed, wsc, nullptr, nullptr, x, m, w->n / e, w->k, e, offsets, y, false, s);
     uint8_t* codes = (uint8_t*)ws;
     uint8_t* scale = codes + mx_x_code_bytes(m, w->k);
-    if ((st = launch_quantize_mxfp4(x, WQ_BF16, m, w->k, scale, nullptr, codes, nullptr, s))) return st;
+    if ((st = launch_quantize_mxfp4(x, WQ_BF16, m, w->k, scale, nullptr, codes, nullptr, true, s))) return st;
     return launch_gemm_mxfp4(w->packed, wsc, codes, scale, nullptr, m, w->n / e, w->k, e, offsets, y, true, s);
 }
 

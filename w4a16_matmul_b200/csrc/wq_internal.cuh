@@ -174,10 +174,11 @@ wq_status launch_wf_gemv(const uint8_t* packed, int64_t packed_bytes, const uint
 wq_status read_wf_error(int32_t* code);
 
 // MXFP4 (wq_mx.cu, wq_mx_gemm.cu). A row's scale bytes are padded to whole 16 bytes, so that
-// every row starts where a 128-bit load or a TMA box may.
+// every row starts where a 128-bit load or a TMA box may. early: the next kernel is a product
+// launched with overlap.
 __host__ __device__ constexpr int64_t mx_pitch(int64_t k) { return (k + 511) / 512 * 16; }
 wq_status launch_quantize_mxfp4(const void* x, int dtype, int64_t n, int64_t k, uint8_t* scale, uint8_t* codes,
-                                uint8_t* packed, void* q, cudaStream_t s);
+                                uint8_t* packed, void* q, bool early, cudaStream_t s);
 wq_status launch_dequant_mxfp4(const wq_weight& w, uint16_t* out, cudaStream_t s);
 // y = x W^T for MXFP4 x [m, k] and W [experts * n, k]: rows [offsets[e], offsets[e + 1]) of x
 // with the n rows of expert e; offsets NULL (experts 1): all rows. x is given as codes and scale

@@ -120,11 +120,13 @@ template <bool F32, typename I>
 __global__ void __launch_bounds__(kThreads)
 quantize_mxfp4_kernel(const void* __restrict__ x, I n_chunks, uint32_t kb, uint32_t pitch,
                       uint8_t* __restrict__ scale, uint2* __restrict__ codes, uint32_t* __restrict__ packed,
-                      void* __restrict__ q) {
+                      void* __restrict__ q, bool early) {
     constexpr int U = 2;
     constexpr uint32_t PER = 8 * U;                            // blocks of a warp's trip, consecutive
-    // a kernel launched to overlap this one may start; it waits before it reads what this writes
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // in front of a product (which waits before it reads what this writes): it may start. Not for
+    // a caller's own quantisation: an overlapped GEMV plan two launches later would load weights
+    // that are still being written here.
+    if (early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const I stride = (I)gridDim.x * blockDim.x * U;
     const I lane = threadIdx.x & 31;
     // a warp covers U consecutive runs of 32 chunks; a block never straddles n_chunks
@@ -199,7 +201,7 @@ dequant_mxfp4_kernel(const uint32_t* __restrict__ packed, const uint8_t* __restr
 }  // namespace
 
 wq_status launch_quantize_mxfp4(const void* x, int dtype, int64_t n, int64_t k, uint8_t* scale, uint8_t* codes,
-                                uint8_t* packed, void* q, cudaStream_t s) {
+                                uint8_t* packed, void* q, bool early, cudaStream_t s) {
     const int64_t chunks = n * k / 8;
     constexpr int U = 2;
     const int grid = stream_grid((chunks + U - 1) / U);
@@ -208,7 +210,7 @@ wq_status launch_quantize_mxfp4(const void* x, int dtype, int64_t n, int64_t k, 
     const bool narrow = chunks + (int64_t)grid * kThreads * U < (int64_t)1 << 32;
 #define WQ_MXQ(F32, I)                                                                                     \
     quantize_mxfp4_kernel<F32, I><<<grid, kThreads, 0, s>>>(x, (I)chunks, kb, pitch, scale, (uint2*)codes, \
-                                                            (uint32_t*)packed, q)
+                                                            (uint32_t*)packed, q, early)
     if (dtype == WQ_F32) {
         if (narrow) WQ_MXQ(true, uint32_t); else WQ_MXQ(true, uint64_t);
     } else {
