@@ -223,6 +223,16 @@ def test_product(wq, m, n, k):
     assert wq.device_error() == 0
 
 
+@pytest.mark.parametrize("m, n, k", [(1, 20000, 512), (5, 20000, 2112), (8, 19000, 576), (9, 20000, 1088)])
+def test_product_of_few_rows_over_all_of_k(wq, m, n, k):
+    """So many weight rows that no CTA splits K: one to five scale stages each."""
+    codes, scale = weights(n, k, n + k)
+    x = acts(m, k, m)
+    xc, xs = mx.quantize(x.double().numpy())
+    check(wq.gemm_mxfp4(packed(wq, codes, scale), x.cuda()), mx.values(xc, xs), mx.values(codes, scale))
+    assert wq.device_error() == 0
+
+
 @pytest.mark.parametrize("m, n, k", [(127, 300, 832), (128, 128, 4096), (129, 500, 1088), (255, 129, 320),
                                      (256, 256, 2048), (257, 1003, 2112), (1000, 640, 512), (4096, 384, 1024)])
 def test_product_large(wq, m, n, k):
@@ -249,6 +259,7 @@ def experts_ref(xv, wv, off, n):
     ([16, 17, 1, 0, 15, 33], 200, 1088), ([130, 0, 1, 257, 64], 300, 192), ([500, 3], 129, 1024),
     ([1] * 70, 64, 256), ([0] * 40 + [2] + [0] * 30 + [9], 33, 320), ([300, 0, 290, 310], 384, 512),
     ([0, 3, 0] * 100 + [40] + [1] * 33, 16, 64), ([0] * 500 + [5] + [0] * 523, 8, 64), ([200] * 40, 24, 64),
+    ([0] * 20 + [37] + [0] * 10 + [18] + [0] * 40, 200, 1088), ([8], 130, 2112), ([9], 130, 2112), ([4, 4], 20, 576),
 ])
 def test_experts(wq, counts, n, k):
     e, t = len(counts), sum(counts)
@@ -334,7 +345,7 @@ def test_nan_blocks_reach_their_rows_and_columns_only(wq):
     codes, scale = weights(n, k, 1)
     scale[77, 3] = 255
     pw = packed(wq, codes, scale)
-    for m in (9, 50, 300):
+    for m in (5, 9, 50, 300):
         x = acts(m, k, m)
         x[m // 2, 100] = float("inf")
         y = wq.gemm_mxfp4(pw, x.cuda()).float().cpu().numpy()

@@ -61,7 +61,8 @@ def test_workspace_bytes(wq):
     # codes rounded up to 256 bytes, then the scale rows of whole 16 bytes
     assert f(100, 4096) == 100 * 2048 + 100 * 128
     assert f(33, 64) == 1280 + 33 * 16
-    assert f(32, 4096) == f(1, 64) == 0 and f(256, 4096, 8) == 0 and f(257, 4096, 8) > 0
+    assert f(8, 4096) == f(1, 64) == 0 and f(9, 4096) == 9 * 2048 + 9 * 128
+    assert f(8, 4096, 2) == f(64, 4096, 64) == 0 and f(65, 4096, 64) == f(65, 4096)
     assert wq._lib.wq_gemm_mxfp4_workspace_bytes(0, 64, 0) == 0
     assert wq._lib.wq_gemm_mxfp4_workspace_bytes(64, 64, -1) == 0
 

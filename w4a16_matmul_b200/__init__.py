@@ -497,7 +497,7 @@ def gemm_mxfp4(w: PackedWeight, x, out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y = x W^T with both operands MXFP4, on the block-scaled tensor cores -> bf16 [m, n]. x is
     quantize_mxfp4's result for [m, k] activations, or a bf16 [m, k] tensor, which is quantised
-    on the way (more than 32 rows: into `workspace`, allocated if not given). k % 64 == 0."""
+    on the way (more than 8 rows: into `workspace`, allocated if not given). k % 64 == 0."""
     return _mx_product(w, x, out, workspace, None)
 
 

@@ -170,23 +170,21 @@ __device__ __forceinline__ void skip_experts(const int32_t* __restrict__ offsets
     at.before = __shfl_sync(0xFFFFFFFFu, incl - tiles, f);
 }
 
-// Activations as they come, for tiles of at most 32 rows (XQ): warps 2-5 quantise them on the way
-// into the stage, a block of 32 columns a thread at a time, one scale stage ahead in registers.
-// Every CTA of a row tile repeats that work, which few rows make cheap; it saves the kernel in
-// front, its workspace, and the wait for it.
-template <int BN>
+// Activations as they come, for few rows (XQ): warps 2-5 quantise them on the way into the stage,
+// a block of 32 columns a thread at a time, one or two scale stages ahead in registers. Every CTA
+// of a row tile repeats that work; it saves the kernel in front, its workspace, and the wait for
+// it (mx_quantises_itself says up to how many rows that pays).
 struct XBlocks {
-    static constexpr int PER = BN * 16 / 128;    // blocks of 32 a thread has in a scale stage of 512 columns
+    static constexpr int PER = 2;                // blocks of 32 a thread has in 16 rows x 512 columns
     uint4 v[PER][4];
 };
 // Block j of thread m (0..127): activation row 8 j + m / 16, columns 32 (m % 16) .. + 31. Rows
 // from `rows` on are left out: what their accumulator columns hold is not stored.
-template <int BN>
-__device__ __forceinline__ void load_x_blocks(XBlocks<BN>& xb, const uint16_t* __restrict__ x, int m, int t0, int rows,
+__device__ __forceinline__ void load_x_blocks(XBlocks& xb, const uint16_t* __restrict__ x, int m, int t0, int rows,
                                               int col0, int K) {
     const int col = col0 + 32 * (m % 16);
 #pragma unroll
-    for (int j = 0; j < XBlocks<BN>::PER; ++j) {
+    for (int j = 0; j < XBlocks::PER; ++j) {
         const int row = 8 * j + m / 16;
         const uint16_t* p = x + (size_t)(t0 + row) * K + col;
 #pragma unroll
@@ -232,7 +230,10 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_xs,
                const uint16_t* __restrict__ x16, const int32_t* __restrict__ offsets, int experts,
                uint16_t* __restrict__ y, int M, int N, int K, int grid_n, int kt_per_split) {
-    static_assert(!XQ || BN <= 32, "few rows");
+    static_assert(!XQ || BN == 16, "few rows");
+    // scale stages the activations are loaded ahead: two where a CTA walks all of K (28672 x 8192 at
+    // 8 rows: 29.0 us one ahead, 25.0 two), one for experts (64 rows on 64 of 1408 x 2048: 19.4 / 21.2)
+    constexpr int AHEAD = EXPERTS ? 1 : 2;
     using C = Cfg<BN>;
     constexpr uint32_t kScTx = XQ ? BM * 16 : C::SC_BYTES, kCodeTx = XQ ? C::A_BYTES : C::STAGE;
     constexpr int STAGES = C::STAGES, SS = C::SSTAGES, TS = C::TSLOTS;
@@ -301,8 +302,11 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     const int nk = max(0, min(KT, kt0 + kt_per_split) - kt0);
     const int t0 = tile.t0, tend = tile.tend;
     const int w0 = tile.expert * N + n0;                         // first weight row of the tile in the stack
-    XBlocks<XQ ? BN : 16> xb;
-    if (XQ && warp >= 2) load_x_blocks(xb, x16, (int)threadIdx.x - 64, t0, tend - t0, kt0 * KB, K);
+    XBlocks xb0, xb1;                                            // of the scale stages in turn
+    if (XQ && warp >= 2) {
+        load_x_blocks(xb0, x16, (int)threadIdx.x - 64, t0, tend - t0, kt0 * KB, K);
+        if (AHEAD == 2 && nk > 2) load_x_blocks(xb1, x16, (int)threadIdx.x - 64, t0, tend - t0, (kt0 + 2) * KB, K);
+    }
 
     auto stage_a = [&](int s) { return smem + s * C::STAGE; };
     auto stage_b = [&](int s) { return smem + s * C::STAGE + C::A_BYTES; };
@@ -410,7 +414,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         int ss = 0, t = 0, cs = 0;                                // scale stage, slot, code stage (XQ)
         uint32_t sph = 0, tph = 0, cph = 0;
         const int nt = (nk + 1) / 2;
-        for (int it = 0; it < nt; ++it) {
+        auto move = [&](int it, XBlocks& xb) {
             bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sfull[ss], sph, s_abort) &&
                                               (it < TS || mbar_wait(&tfree[t], tph ^ 1, s_abort)));
             if (XQ) {
@@ -425,7 +429,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                 if (ok && (b < 8 || two)) {
                     uint8_t* tile_b = stage_b(b < 8 ? cs : cs1);
 #pragma unroll
-                    for (int j = 0; j < XBlocks<BN>::PER; ++j) {
+                    for (int j = 0; j < XBlocks::PER; ++j) {
                         const int row = 8 * j + m / 16;
                         if (t0 + row < tend) {
                             uint4 codes;
@@ -439,11 +443,12 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                 cs = cs1 + 1;
                 cph = cph1;
                 if (cs == STAGES) { cs = 0; cph ^= 1; }
-                if (it + 1 < nt) load_x_blocks(xb, x16, m, t0, tend - t0, kt0 * KB + (it + 1) * 2 * KB, K);
+                if (it + AHEAD < nt)
+                    load_x_blocks(xb, x16, m, t0, tend - t0, (kt0 + 2 * (it + AHEAD)) * KB, K);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMAs read the codes
                 ok = bar_all(1, 128, ok);                         // warps 2-5
             }
-            if (!ok) { dead(2205); break; }
+            if (!ok) { dead(2205); return false; }
             const uint4* sc = (const uint4*)stage_sc(ss);
             uint32_t v[C::SLOT_COLS];
 #pragma unroll
@@ -462,6 +467,11 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             if (lane == 0) { mbar_arrive(&sempty[ss]); mbar_arrive(&tfull[t]); }
             if (++ss == SS) { ss = 0; sph ^= 1; }
             if (++t == TS) { t = 0; tph ^= 1; }
+            return true;
+        };
+        for (int it = 0; it < nt; ++it) {
+            if (!move(it, xb0)) break;
+            if (XQ && AHEAD == 2 && (++it == nt || !move(it, xb1))) break;
         }
         const bool drain = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0)) &&
                            !__any_sync(0xFFFFFFFFu, *(volatile int*)s_abort != 0);
@@ -1039,7 +1049,12 @@ wq_status launch_pair(const Maps& mp, const int32_t* offsets, int experts, uint1
 
 }  // namespace
 
-bool mx_quantises_itself(int64_t m, int experts) { return (m + experts - 1) / experts <= 32; }
+// Few rows are quantised by the product (XQ), more by a kernel in front, which costs 0.5 to 0.9 us
+// (and 4 us of host time) once, where XQ repeats the work in every tile. XQ / kernel in front:
+//   4096 x 4096 at 1, 8, 16, 32 rows: 5.7 / 6.6, 5.9 / 6.6, 6.9 / 6.6, 8.8 / 7.6 us; 28672 x 8192
+//   at 1, 8, 16, 32: 23.7 / 25.5, 25.0 / 24.6, 31.9 / 24.8, 45.8 / 25.5; 64 experts of 1408 x 2048
+//   at 1/2, 1, 2, 8 rows each: 12.0 / 12.7, 19.4 / 20.8, 26.7 / 26.0, 33.5 / 28.5
+bool mx_quantises_itself(int64_t m, int experts) { return m <= std::max(8, experts); }
 
 wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t* xp, const uint8_t* xsc,
                             const uint16_t* x16, int64_t m, int64_t n, int64_t k, int experts, const int32_t* offsets,
@@ -1100,7 +1115,7 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
              : cl == 2 ? WQ_MX(BN, 2, false, XQ) : WQ_MX(BN, 1, false, XQ))
     switch (bn) {
         case 16: return x16 ? WQ_MX_CL(16, true) : WQ_MX_CL(16, false);
-        case 32: return x16 ? WQ_MX_CL(32, true) : WQ_MX_CL(32, false);
+        case 32: return WQ_MX_CL(32, false);
         case 64: return WQ_MX_CL(64, false);
         default: return WQ_MX_CL(128, false);
     }
