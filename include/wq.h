@@ -332,7 +332,7 @@ wq_status wq_gemm_w4a16(const wq_weight* w, const uint16_t* x, int64_t m, uint16
 
 /* Bytes of device workspace the _bf16 forms below need for the codes and scale bytes of m rows
  * of k activations, in a product grouped by `experts` (0: the dense product). 0 for up to 8
- * rows, and for no more rows than experts, where the product quantises them itself. */
+ * rows, and for no more rows than half the experts, where the product quantises them itself. */
 size_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t k, int32_t experts);
 
 /* The product of two MXFP4 matrices on the block-scaled tensor cores (tcgen05 kind::mxf4):

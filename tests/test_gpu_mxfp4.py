@@ -259,7 +259,7 @@ def experts_ref(xv, wv, off, n):
     ([16, 17, 1, 0, 15, 33], 200, 1088), ([130, 0, 1, 257, 64], 300, 192), ([500, 3], 129, 1024),
     ([1] * 70, 64, 256), ([0] * 40 + [2] + [0] * 30 + [9], 33, 320), ([300, 0, 290, 310], 384, 512),
     ([0, 3, 0] * 100 + [40] + [1] * 33, 16, 64), ([0] * 500 + [5] + [0] * 523, 8, 64), ([200] * 40, 24, 64),
-    ([0] * 20 + [37] + [0] * 10 + [18] + [0] * 40, 200, 1088), ([8], 130, 2112), ([9], 130, 2112), ([4, 4], 20, 576),
+    ([0] * 20 + [37] + [0] * 80 + [18] + [0] * 40, 200, 1088), ([8], 130, 2112), ([9], 130, 2112), ([4, 4], 20, 576),
 ])
 def test_experts(wq, counts, n, k):
     e, t = len(counts), sum(counts)

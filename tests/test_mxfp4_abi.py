@@ -62,7 +62,7 @@ def test_workspace_bytes(wq):
     assert f(100, 4096) == 100 * 2048 + 100 * 128
     assert f(33, 64) == 1280 + 33 * 16
     assert f(8, 4096) == f(1, 64) == 0 and f(9, 4096) == 9 * 2048 + 9 * 128
-    assert f(8, 4096, 2) == f(64, 4096, 64) == 0 and f(65, 4096, 64) == f(65, 4096)
+    assert f(8, 4096, 2) == f(32, 4096, 64) == 0 and f(33, 4096, 64) == f(33, 4096)
     assert wq._lib.wq_gemm_mxfp4_workspace_bytes(0, 64, 0) == 0
     assert wq._lib.wq_gemm_mxfp4_workspace_bytes(64, 64, -1) == 0
 

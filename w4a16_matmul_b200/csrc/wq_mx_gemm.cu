@@ -15,7 +15,7 @@
 //              128 columns in lane r % 32 of column r / 32, in each of the four lane quarters,
 //              so each warp fills its own quarter; afterwards they drain the accumulator. For few
 //              rows they quantise the activations, too (XQ below).
-// Up to 128 activation rows (of an expert, on average) run this way; more run on pairs of CTAs,
+// Up to 128 activation rows run this way, and few rows of experts; the rest runs on pairs of CTAs,
 // the second kernel below.
 // Grouped by expert, a CTA finds its expert and its rows from the offsets on the device: the
 // host reads nothing back, and launches as many row tiles as the worst distribution needs.
@@ -671,6 +671,7 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         atomicCAS(&g_mx_error, 0, code);
     };
     MxScan at;
+    if (EXPERTS && experts > 64) skip_experts(offsets, experts, M, (int)blockIdx.x / 2 / grid_n, bn, at);
     // tile number `lin`: its weight-row tile nt (fastest) and its activation rows; false: none
     auto get = [&](int lin, int& n0, MxTile& t) {
         n0 = (lin % grid_n) * 256 + rank * BM;
@@ -1053,8 +1054,8 @@ wq_status launch_pair(const Maps& mp, const int32_t* offsets, int experts, uint1
 // (and 4 us of host time) once, where XQ repeats the work in every tile. XQ / kernel in front:
 //   4096 x 4096 at 1, 8, 16, 32 rows: 5.7 / 6.6, 5.9 / 6.6, 6.9 / 6.6, 8.8 / 7.6 us; 28672 x 8192
 //   at 1, 8, 16, 32: 23.7 / 25.5, 25.0 / 24.6, 31.9 / 24.8, 45.8 / 25.5; 64 experts of 1408 x 2048
-//   at 1/2, 1, 2, 8 rows each: 12.0 / 12.7, 19.4 / 20.8, 26.7 / 26.0, 33.5 / 28.5
-bool mx_quantises_itself(int64_t m, int experts) { return m <= std::max(8, experts); }
+//   at 1/2, 3/4, 1 rows each: 12.0 / 13.5, 17.8 / 16.1, 19.5 / 18.3
+bool mx_quantises_itself(int64_t m, int experts) { return m <= std::max(8, experts / 2); }
 
 wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t* xp, const uint8_t* xsc,
                             const uint16_t* x16, int64_t m, int64_t n, int64_t k, int experts, const int32_t* offsets,
@@ -1068,9 +1069,16 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
     Maps mp;
     const int64_t pitch = mx_pitch(k);
     wq_status st;
-    if (rows > 128) {
+    // Pairs for many rows, and for experts unless the kernel quantises x: their persistent grid walks
+    // the tiles that there are, and takes wide tiles at little cost (32 experts of 5632 x 2048 at 2 /
+    // 8 / 32 / 128 rows each: 42.9 / 51.4 / 69.2 / 88.9 us one CTA a tile of the average's width,
+    // 40.2 / 41.0 / 41.8 / 51.9 in pairs). Experts have more or fewer rows than the average: room for
+    // half as many again, which spares most of them a second tile (at 32 / 64 / 128 rows: 46.6 /
+    // 48.8 / 55.9 us without, 41.9 / 44.5 / 55.5 with as many again).
+    if (!x16 && (offsets || rows > 128)) {
         const int gn = (N + 255) / 256;
-        const int bn = pair_width(rows, (int64_t)gn * experts, sms / 2);
+        const int64_t room = offsets ? std::max(rows, std::min<int64_t>(rows + rows / 2, 256)) : rows;
+        const int bn = pair_width(room, (int64_t)gn * experts, sms / 2);
         const int64_t gm = offsets ? m / bn + std::min<int64_t>(experts, m) : (m + bn - 1) / bn;
         if (gm * gn > 0x3FFFFFFF) return fail(WQ_EUNSUPPORTED, "more than 2^30 - 1 tiles");
         if ((st = encode_u8(&mp.w, wp, k / 2, n * experts, KB / 2, BM, true, "the weight codes"))) return st;
@@ -1110,9 +1118,10 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
     }
 #define WQ_MX(BN, CL, EX, XQ) \
     launch_one<BN, CL, EX, XQ>(mp, x16, offsets, experts, y, M, N, K, grid_n, grid_m, per, overlap, s)
-#define WQ_MX_CL(BN, XQ)                                                                           \
-    (offsets ? WQ_MX(BN, 1, true, XQ) : cl == 8 ? WQ_MX(BN, 8, false, XQ) : cl == 4 ? WQ_MX(BN, 4, false, XQ) \
+#define WQ_MX_CL(BN, XQ)                                                         \
+    (cl == 8 ? WQ_MX(BN, 8, false, XQ) : cl == 4 ? WQ_MX(BN, 4, false, XQ)       \
              : cl == 2 ? WQ_MX(BN, 2, false, XQ) : WQ_MX(BN, 1, false, XQ))
+    if (offsets) return WQ_MX(16, 1, true, true);                // at most 8 rows an expert on average
     switch (bn) {
         case 16: return x16 ? WQ_MX_CL(16, true) : WQ_MX_CL(16, false);
         case 32: return WQ_MX_CL(32, false);
