@@ -15,8 +15,8 @@
 //              128 columns in lane r % 32 of column r / 32, in each of the four lane quarters,
 //              so each warp fills its own quarter; afterwards they drain the accumulator. For few
 //              rows they quantise the activations, too (XQ below).
-// Up to 128 activation rows run this way, and few rows of experts; the rest runs on pairs of CTAs,
-// the second kernel below.
+// Few activation rows run this way; more, and most products of experts, run on pairs of CTAs, the
+// second kernel below (launch_gemm_mxfp4 says when).
 // Grouped by expert, a CTA finds its expert and its rows from the offsets on the device: the
 // host reads nothing back, and launches as many row tiles as the worst distribution needs.
 // Rows of the activation tile past the expert's range belong to the next expert (or lie behind
@@ -1069,13 +1069,34 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
     Maps mp;
     const int64_t pitch = mx_pitch(k);
     wq_status st;
+    const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    // row tiles: with experts the most that any distribution of the rows needs
+    const int64_t grid_m = offsets ? m / bn + std::min<int64_t>(experts, m) : (m + bn - 1) / bn;
+    if (grid_m * grid_n > 0x7FFFFFFF) return fail(WQ_EUNSUPPORTED, "more than 2^31 - 1 tiles");
+    // K split over a cluster: one CTA an SM as long as each keeps 512 columns, two while each
+    // keeps 1024 (4096 x 4096 at one row, 32 tiles: 9.0 / 6.8 / 6.0 / 6.7 us at 1 / 2 / 4 / 8 ranks)
+    int cl = 1;
+    if (!offsets)
+        while (cl < 8) {
+            const int64_t ctas = grid_m * grid_n * cl * 2;
+            const int stages = KT / (cl * 2);
+            if (!((ctas <= sms && stages >= 2) || (ctas <= 2 * (int64_t)sms && stages >= 4))) break;
+            cl *= 2;
+        }
     // Pairs for many rows, and for experts unless the kernel quantises x: their persistent grid walks
     // the tiles that there are, and takes wide tiles at little cost (32 experts of 5632 x 2048 at 2 /
     // 8 / 32 / 128 rows each: 42.9 / 51.4 / 69.2 / 88.9 us one CTA a tile of the average's width,
     // 40.2 / 41.0 / 41.8 / 51.9 in pairs). Experts have more or fewer rows than the average: room for
     // half as many again, which spares most of them a second tile (at 32 / 64 / 128 rows: 46.6 /
-    // 48.8 / 55.9 us without, 41.9 / 44.5 / 55.5 with as many again).
-    if (!x16 && (offsets || rows > 128)) {
+    // 48.8 / 55.9 us without, 41.9 / 44.5 / 55.5 with as many again). From 33 rows on also where K is
+    // short or cannot be split, as a pair takes all of K in turn: one CTA a tile / pairs, 128 rows of
+    // 5632 x 2048 9.9 / 7.6 us (64 rows 7.6 / 6.7, 33: 6.8 / 6.5), of 11008 x 4096 13.1 / 9.6 (64:
+    // 10.4 / 8.6), of 4096 x 4096 8.6 / 8.2 (64: 7.1 / 8.1), of 4096 x 11008 13.0 / 13.9; 77 rows of
+    // 28672 x 8192 31.6 / 27.6 (64: 25.5 / 26.9), 33 of 20000 x 192 6.1 / 7.7 (77: 7.9 / 8.4; 77 of
+    // 1024 x 1024 7.4 / 5.8).
+    const bool pairs = offsets || rows > 128 || (rows > 64 && (cl == 1 || K <= 4096)) ||
+                       (rows > 32 && cl <= 2 && K > 512 && K <= 4096);
+    if (!x16 && pairs) {
         const int gn = (N + 255) / 256;
         const int64_t room = offsets ? std::max(rows, std::min<int64_t>(rows + rows / 2, 256)) : rows;
         const int bn = pair_width(room, (int64_t)gn * experts, sms / 2);
@@ -1092,20 +1113,6 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
         return offsets ? launch_pair<true>(mp, offsets, experts, y, M, N, K, gn, (int)gm, bn, overlap, s)
                        : launch_pair<false>(mp, offsets, experts, y, M, N, K, gn, (int)gm, bn, overlap, s);
     }
-    const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    // row tiles: with experts the most that any distribution of the rows needs
-    const int64_t grid_m = offsets ? m / bn + std::min<int64_t>(experts, m) : (m + bn - 1) / bn;
-    if (grid_m * grid_n > 0x7FFFFFFF) return fail(WQ_EUNSUPPORTED, "more than 2^31 - 1 tiles");
-    // K split over a cluster: one CTA an SM as long as each keeps 512 columns, two while each
-    // keeps 1024 (4096 x 4096 at one row, 32 tiles: 9.0 / 6.8 / 6.0 / 6.7 us at 1 / 2 / 4 / 8 ranks)
-    int cl = 1;
-    if (!offsets)
-        while (cl < 8) {
-            const int64_t ctas = grid_m * grid_n * cl * 2;
-            const int stages = KT / (cl * 2);
-            if (!((ctas <= sms && stages >= 2) || (ctas <= 2 * (int64_t)sms && stages >= 4))) break;
-            cl *= 2;
-        }
     int per = (KT + cl - 1) / cl;
     per += per & 1;
     if ((st = encode_u8(&mp.w, wp, k / 2, n * experts, KB / 2, BM, true, "the weight codes"))) return st;
@@ -1126,7 +1133,9 @@ wq_status launch_gemm_mxfp4(const uint8_t* wp, const uint8_t* wsc, const uint8_t
         case 16: return x16 ? WQ_MX_CL(16, true) : WQ_MX_CL(16, false);
         case 32: return WQ_MX_CL(32, false);
         case 64: return WQ_MX_CL(64, false);
-        default: return WQ_MX_CL(128, false);
+        default:                                                 // (unsplit: pairs)
+            return cl == 8 ? WQ_MX(128, 8, false, false) : cl == 4 ? WQ_MX(128, 4, false, false)
+                                                                   : WQ_MX(128, 2, false, false);
     }
 #undef WQ_MX_CL
 #undef WQ_MX
