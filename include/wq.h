@@ -27,6 +27,8 @@
  *   - Arguments are checked on the host before anything is launched; on any failure
  *     nothing is launched and the status says why (details in wq_last_error()). A launch
  *     failure reported by the CUDA runtime returns WQ_ECUDA.
+ *   - Rows and columns of a matrix are at most 2^31 - 1; of a packed weight that is multiplied
+ *     (the wq_gemv_w4a16 and wq_gemm entries), and of an MXFP4 activation's columns, 2^31 - 1024.
  *   - Inputs must be finite. NaN or Inf weights or activations give unspecified codes
  *     and outputs (never a fault).
  *   - Entry points are reentrant; concurrent calls on different streams are safe.

@@ -95,6 +95,15 @@ wq_status check_shape(int64_t n, int64_t k, int64_t group) {
     return WQ_OK;
 }
 
+// The products' kernels number rows and columns in 32 bits and go past n and k to whole tiles and
+// steps, by less than 1024.
+constexpr int64_t kMaxProductSize = (1LL << 31) - 1024;
+wq_status check_product_size(const wq_weight* w) {
+    if (!w || (w->n <= kMaxProductSize && w->k <= kMaxProductSize)) return WQ_OK;
+    return fail(WQ_EINVAL, "a product's n=%lld and k=%lld must not exceed 2^31 - 1024", (long long)w->n,
+                (long long)w->k);
+}
+
 wq_status check_weight(const wq_weight* w) {
     if (!w) return fail(WQ_EINVAL, "weight descriptor is NULL");
     if (w->fmt == WQ_FMT_DYADIC4) {
@@ -129,8 +138,8 @@ wq_status check_bf16x_shape(int64_t n, int64_t k) {
 wq_status gemm_checked(const wq_weight* w, const uint16_t* x, int64_t m, uint16_t* y, void* ws,
                        size_t ws_bytes, cudaStream_t stream, size_t tail_cap) {
     g_last_error[0] = 0;
-    wq_status st = check_weight(w);
-    if (st) return st;
+    wq_status st = check_product_size(w);
+    if (st || (st = check_weight(w))) return st;
     if (w->k % 64 != 0) return fail(WQ_EINVAL, "GEMM needs k %% 64 == 0 (k=%lld)", (long long)w->k);
     if (m < 1 || m > (1LL << 31) - 1) return fail(WQ_EINVAL, "m=%lld outside 1..2^31-1", (long long)m);
     if ((st = check_ptr(x, "x", false))) return st;
@@ -436,8 +445,8 @@ wq_status check_grouped(const wq_weight* ws, const uint16_t* const* xs, uint16_t
         return fail(WQ_EINVAL, "count=%d outside 1..%d", count, WQ_GEMV_MAX_GROUPED);
     if (batch < 1 || batch > 16) return fail(WQ_EINVAL, "batch=%d outside 1..16", batch);
     for (int i = 0; i < count; ++i) {
-        wq_status st = check_weight(&ws[i]);
-        if (st) return st;
+        wq_status st = check_product_size(&ws[i]);
+        if (st || (st = check_weight(&ws[i]))) return st;
         if (ws[i].fmt != ws[0].fmt || ws[i].group != ws[0].group)
             return fail(WQ_EINVAL, "problem %d: all grouped weights must share format and group", i);
         if ((st = check_ptr(xs[i], "x", false))) return st;
@@ -558,8 +567,8 @@ size_t mx_x_code_bytes(int64_t m, int64_t k) { return ((size_t)m * (size_t)(k / 
 wq_status check_mx(const wq_weight* w, const char* name) {
     if (!w) return fail(WQ_EINVAL, "%s descriptor is NULL", name);
     if (w->fmt != WQ_FMT_MXFP4) return fail(WQ_EINVAL, "%s must be MXFP4 (got format %d)", name, w->fmt);
-    wq_status st = check_weight(w);
-    if (st) return st;
+    wq_status st = check_product_size(w);
+    if (st || (st = check_weight(w))) return st;
     if (w->k % 64 != 0) return fail(WQ_EINVAL, "MXFP4 products need k %% 64 == 0 (k=%lld)", (long long)w->k);
     return WQ_OK;
 }
