@@ -328,6 +328,13 @@ def dequant(w: PackedWeight, out: torch.Tensor | None = None) -> torch.Tensor:
 
 # --- consumers ---------------------------------------------------------------------------
 
+def _output(out: torch.Tensor, rows: int, cols: int, name: str) -> torch.Tensor:
+    """The caller's buffer for a product: as many bf16 values at least as are written."""
+    if _cuda(out, torch.bfloat16, name).numel() < rows * cols:
+        raise ValueError(f"{name} must hold [{rows}, {cols}]")
+    return out
+
+
 def gemv(w: PackedWeight, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     """y = Wdeq x for x bf16 [batch, k] (batch <= 16) -> bf16 [batch, n]. A CPU x is copied to
     the weight's device (pinned, non-blocking) and the result copied back."""
@@ -336,8 +343,10 @@ def gemv(w: PackedWeight, x: torch.Tensor, out: torch.Tensor | None = None) -> t
         x = x.pin_memory().to(w.packed.device, non_blocking=True) if x.device.type == "cpu" else x
     x2 = x if x.dim() == 2 else x.reshape(1, -1)
     _cuda(x2, torch.bfloat16, "x")
-    b = x2.shape[0]
-    y = out if out is not None else _matrix(b, w.n, torch.bfloat16, x2.device)
+    b, k = x2.shape
+    if k != w.k:
+        raise ValueError(f"x has {k} columns, w has {w.k}")
+    y = _matrix(b, w.n, torch.bfloat16, x2.device) if out is None else _output(out, b, w.n, "out")
     d = w.desc()
     _check(_lib.wq_gemv_w4a16(ctypes.byref(d), _ptr(x2), b, _ptr(y), _stream(x2)))
     if host:
@@ -345,13 +354,24 @@ def gemv(w: PackedWeight, x: torch.Tensor, out: torch.Tensor | None = None) -> t
     return y if x.dim() == 2 else y.reshape(-1)
 
 
+def _grouped_batch(ws, xs, ys) -> int:
+    """Checks a grouped GEMV's x [batch, k] and, if given, y [batch, n]; returns the batch."""
+    if not ws or len(xs) != len(ws) or (ys is not None and len(ys) != len(ws)):
+        raise ValueError("ws, xs and ys must have the same length, at least 1")
+    b = xs[0].shape[0]
+    for i, (w, x) in enumerate(zip(ws, xs)):
+        if _cuda(x, torch.bfloat16, "x").numel() != b * w.k:
+            raise ValueError(f"x of problem {i} must be [{b}, {w.k}], got {tuple(x.shape)}")
+        if ys is not None:
+            _output(ys[i], b, w.n, "y")
+    return b
+
+
 def gemv_grouped(ws: list[PackedWeight], xs: list[torch.Tensor],
                  ys: list[torch.Tensor] | None = None) -> list[torch.Tensor]:
     """Independent GEMVs ys[i] = Wdeq(ws[i]) xs[i] in one launch (same format/group/batch)."""
     cnt = len(ws)
-    b = xs[0].shape[0]
-    for x in xs:
-        _cuda(x, torch.bfloat16, "x")
+    b = _grouped_batch(ws, xs, ys)
     if ys is None:
         ys = [torch.empty((b, w.n), dtype=torch.bfloat16, device=xs[0].device) for w in ws]
     arr = (WqWeight * cnt)(*[w.desc() for w in ws])
@@ -371,14 +391,8 @@ class GroupedGemv:
 
     def __init__(self, ws: list[PackedWeight], xs: list[torch.Tensor], ys: list[torch.Tensor],
                  overlap: bool = False):
-        if not (len(ws) == len(xs) == len(ys)):
-            raise ValueError("ws, xs and ys must have the same length")
-        for x in xs:
-            _cuda(x, torch.bfloat16, "x")
-        for y in ys:
-            _cuda(y, torch.bfloat16, "y")
         self.cnt = len(ws)
-        self.batch = xs[0].shape[0]
+        self.batch = _grouped_batch(ws, xs, ys)
         self._keep = (ws, xs, ys)
         arr = (WqWeight * self.cnt)(*[w.desc() for w in ws])
         xp = (_vp * self.cnt)(*[x.data_ptr() for x in xs])
@@ -411,12 +425,19 @@ def gemm_workspace_bytes(w: PackedWeight, m: int) -> int:
     return int(_lib.wq_gemm_workspace_bytes(ctypes.byref(d), m))
 
 
+def _gemm_rows(w: PackedWeight, x: torch.Tensor) -> int:
+    _cuda(x, torch.bfloat16, "x")
+    m = x.shape[0]
+    if x.numel() != m * w.k:
+        raise ValueError(f"x must be [m, {w.k}], got {tuple(x.shape)}")
+    return m
+
+
 def gemm(w: PackedWeight, x: torch.Tensor, out: torch.Tensor | None = None,
          workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y = x Wdeq^T for x bf16 [m, k] -> bf16 [m, n] on the tcgen05 tensor cores."""
-    _cuda(x, torch.bfloat16, "x")
-    m = x.shape[0]
-    y = out if out is not None else _matrix(m, w.n, torch.bfloat16, x.device)
+    m = _gemm_rows(w, x)
+    y = _matrix(m, w.n, torch.bfloat16, x.device) if out is None else _output(out, m, w.n, "out")
     d = w.desc()
     need = int(_lib.wq_gemm_workspace_bytes(ctypes.byref(d), m))
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
@@ -429,9 +450,8 @@ def gemm(w: PackedWeight, x: torch.Tensor, out: torch.Tensor | None = None,
 def gemm_static(w: PackedWeight, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     """gemm() with its scratch in the library's static device array (wq_gemm_w4a16_static):
     no workspace is allocated for the call."""
-    _cuda(x, torch.bfloat16, "x")
-    m = x.shape[0]
-    y = out if out is not None else torch.empty((m, w.n), dtype=torch.bfloat16, device=x.device)
+    m = _gemm_rows(w, x)
+    y = _matrix(m, w.n, torch.bfloat16, x.device) if out is None else _output(out, m, w.n, "out")
     d = w.desc()
     _check(_lib.wq_gemm_w4a16_static(ctypes.byref(d), _ptr(x), m, _ptr(y), _stream(x)))
     return y
@@ -457,7 +477,7 @@ def _mx_product(w: PackedWeight, x, out, workspace, offsets):
             raise ValueError(f"the stack's {w.n} rows are not a multiple of {experts} experts")
     n = w.n // experts if experts else w.n
     if coded:
-        m, k, t = x.n, x.k, x.packed
+        m, k, t = x.n, x.k, _cuda(x.packed, torch.uint8, "x.packed")
     else:
         t = _cuda(x, torch.bfloat16, "x")
         if x.dim() != 2:
