@@ -231,6 +231,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                const uint16_t* __restrict__ x16, const int32_t* __restrict__ offsets, int experts,
                uint16_t* __restrict__ y, int M, int N, int K, int grid_n, int kt_per_split) {
     static_assert(!XQ || BN == 16, "few rows");
+    static_assert(!EXPERTS || XQ, "experts otherwise run in pairs; so a CTA without a tile overlaps no kernel before it");
     // scale stages the activations are loaded ahead: two where a CTA walks all of K (28672 x 8192 at
     // 8 rows: 29.0 us one ahead, 25.0 two), one for experts (64 rows on 64 of 1408 x 2048: 19.4 / 21.2)
     constexpr int AHEAD = EXPERTS ? 1 : 2;
@@ -292,8 +293,6 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         if (tile.expert < 0) {                                   // (clusters are not used here)
             if (warp == 1)
                 asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
-            // not to be complete before the kernel this launch overlaps
-            asm volatile("griddepcontrol.wait;" ::: "memory");
             return;
         }
     }
