@@ -52,7 +52,7 @@ typedef enum wq_status {
     WQ_EALIGN = 2,        /* pointer not 16-byte aligned */
     WQ_EUNSUPPORTED = 3,  /* valid request this library does not implement (e.g. group) */
     WQ_ECUDA = 4,         /* the CUDA runtime reported an error (launch or attribute query) */
-    WQ_ETIMEOUT = 5,      /* a bounded device-side wait gave up (reserved) */
+    WQ_ETIMEOUT = 5,      /* a bounded device-side wait gave up (wq_device_error) */
     WQ_EDATA = 6          /* a kernel found inconsistent encoded data (wq_device_error) */
 } wq_status;
 
@@ -383,7 +383,7 @@ wq_status wq_gemm_mxfp4_experts_bf16(const wq_weight* w, int32_t experts, const 
  * a nonzero code (the GEMV's is 2100, the MXFP4 products' 2201 to 2217); the BF16X kernels
  * record one when an overflow-table index would pass ovf_bytes, and the water-filling kernels one when a block's width is outside 3..5 or its
  * bytes do not fit packed_bytes (2000 dequant, 2001 pack, 2002 GEMV; the access is skipped
- * in every case). *code receives the code (0 = none). Synchronous (copies three ints from
+ * in every case). *code receives the code (0 = none). Synchronous (copies four ints from
  * the device). Returns WQ_ETIMEOUT if a wait had expired, WQ_EDATA for inconsistent BF16X
  * or water-filling data, WQ_OK otherwise.
  * The debug build of the library (libwq_debug.so, compiled with -DWQ_DEBUG=1) also checks

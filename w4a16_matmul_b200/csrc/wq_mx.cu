@@ -12,7 +12,8 @@
 //
 // Both kernels are HBM streams: a thread owns 8 consecutive values (a quarter of a block),
 // its loads and stores are 128 bits wide, and a warp's accesses are contiguous.
-// Measured at 8192 x 28672 bf16, 4.5 bytes a value with q: 6.48 TB/s, what a copy reaches.
+// Measured at 8192 x 28672 bf16, 4.5 bytes a value with q: 164 us, 6.48 TB/s, what a copy reaches;
+// its reconstruction, 2.5 bytes a value: 90 us, 6.6 TB/s.
 #include "wq_internal.cuh"
 
 namespace wq {

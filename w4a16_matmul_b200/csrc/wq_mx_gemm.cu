@@ -540,9 +540,13 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 // rows and half of the activation rows in shared memory and accumulates its 128 weight rows x
 // bn: per MMA of 64 columns it reads (128 + bn / 2) x 32 bytes where a single CTA reads (128 + bn)
 // x 32. At 256 x 256 that is 64 bytes a clock, and the copies into shared memory take as many
-// again, of the 128 there are; a single CTA's 128 x 256 tile would want 192. The MMAs bound the
-// kernel: 131 clocks each (128 by their rate), measured 0.31 us a stage of four at 1.9 GHz; 5.5
-// PFLOP/s over 4096 x 4096 x 11008, at the power limit.
+// again, of the 128 there are; a single CTA's 128 x 256 tile would want 192. There the MMAs bound
+// the main loop: by their rate a stage of four takes 0.27 us at 1.9 GHz (128 clocks each), measured
+// 0.29. Narrower tiles' stages take less, down to a floor that is not the MMAs': 0.26 us at 192
+// wide, 0.20 from 160 down to 32 (9728 weight rows in L2, K 8192 less K 4096). 5.4 PFLOP/s over
+// 4096 x 4096 x 11008 again and again (5.2 on three sets of inputs in turn), at the power limit.
+// With short K the way from tile to tile counts: 8192 x 5632 x 2048 takes 4.4 us a tile, 2.3 of them
+// its eight stages, as the one accumulator is taken out before the next tile's first MMA.
 //   warp 0      TMA producer of its CTA's codes (both CTAs signal the leader's barrier);
 //   warp 1      MMA issuer (the leader's CTA only), commits to both CTAs;
 //   warps 2-5   scale bytes into tensor memory: the CTA's 128 weight rows and all activation rows;
@@ -1010,12 +1014,13 @@ wq_status launch_one(const Maps& mp, const uint16_t* x16, const int32_t* offsets
     return check_launch("mxfp4 gemm");
 }
 
-// Activation rows a tile of the pair kernel: the grid runs in rounds of `pairs` tiles, a tile takes
-// a time of about bn + 400 (an MMA reads its 256 weight rows, and takes 128 clocks, whatever bn;
-// the way out, and the tile's fill, grow with it), and the fewest rounds times that wins. `rows`: of
-// one expert; `columns`: weight tiles of all. Measured at 4096 x 4096 weights: 256 rows 11.3 us in
-// 16 tiles of 256, 8.6 in 64 of 64; 512 rows 11.7 in 32 of 256, 9.8 in 64 of 128; 1024 rows 12.1 in
-// 64 of 256, 14.0 in 128 of 128; 512 rows of 11008 x 4096 17.5 / 15.8 / 18.6 at 256 / 192 / 128.
+// Activation rows a tile of the pair kernel: the grid runs in rounds of `pairs` tiles, and the
+// fewest rounds times (bn + 400) wins. The 400 stand for what does not grow with bn: a tile's fill
+// and way out and the floor of its stages. It is a ranking fitted to the launches below, not the
+// kernel's time (1024 rows: 1.16 times by the clock, 1.6 by the rule). `rows`: of one expert;
+// `columns`: weight tiles of all. Measured at 4096 x 4096 weights: 256 rows 11.3 us in 16 tiles of
+// 256, 8.6 in 64 of 64; 512 rows 11.7 in 32 of 256, 9.8 in 64 of 128; 1024 rows 12.1 in 64 of 256,
+// 14.0 in 128 of 128; 512 rows of 11008 x 4096 17.5 / 15.8 / 18.6 at 256 / 192 / 128.
 int pair_width(int64_t rows, int64_t columns, int64_t pairs) {
     int best = 256;
     int64_t least = -1;
