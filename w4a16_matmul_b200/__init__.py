@@ -282,7 +282,8 @@ def _quantize_mx(x: torch.Tensor, codes: bool, packed: bool, q: bool):
 
 def quantize_mxfp4(x: torch.Tensor, codes: bool = False):
     """MXFP4 quantisation of a bf16 or fp32 [n, k] matrix, k % 32 == 0 (weights, or the
-    activations of gemm_mxfp4): E2M1 codes and one power-of-two scale byte per 32 columns.
+    activations of gemm_mxfp4, whose products want k % 64 == 0): E2M1 codes and one power-of-two
+    scale byte per 32 columns.
     Returns (PackedWeight, codes uint8 [n, k] | None)."""
     _, c, pw, _ = _quantize_mx(x, codes, True, False)
     return pw, c
